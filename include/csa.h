@@ -68,6 +68,8 @@ typedef enum { CSA_F32 = 0, CSA_BF16 = 1, CSA_KV_FP8MIX = 2 } csa_dtype;
 #define CSA_DEV_RANGE 0x8u      /* an MXFP4 block exponent outside [-23, 13] (the
                                    MXFP4 indexer's exact range); that block was
                                    scored with its exponent clamped */
+#define CSA_DEV_NAN 0x10u      /* a NaN among the values to store in the 8-bit KV
+                                   cache; stored as 0 */
 
 typedef struct {
   int m;          /* tokens per compressed entry (CSA m, HCA m') */
@@ -363,6 +365,151 @@ csa_status hca_attend(const csa_params* p, int B, int Q, const int32_t* q_pos,
                       int N, const void* win, const float* win_scale, int W,
                       const int32_t* win_pos0, const float* sink, void* out,
                       void* workspace, size_t ws_bytes, csa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Uncompressed layers with an 8-bit KV cache.  Layers that keep every token
+ * for n_kv KV heads (grouped queries), next to the compressed ones above: the
+ * per-head norm and rotation of queries and keys, the append of new tokens to
+ * the cache, the attention over it, and the eviction of the token blocks that
+ * received the least attention.  No page counterpart: the calls use the
+ * pages' RMSNorm, RoPE, sink logit and E4M3 storage in the forms that
+ * grouped-query layers take.
+ *
+ * Cache format.  Per sequence and KV head N slots of d OCP E4M3 codes for the
+ * keys and for the values, [B][n_kv][N][d], and one exponent byte for every
+ * `block` consecutive slots, [B][n_kv][N/block] (E8M0: e + 127).  A stored
+ * value is code * 2^e.  e is the least integer with max|x| <= 448 * 2^e over
+ * the finite values of the block, at least -110 (also for a block of zeros)
+ * and at most 119; a code is x * 2^-e rounded to the nearest E4M3 value (ties
+ * to even, saturating at +-448; a NaN is stored as 0 and raises CSA_DEV_NAN).
+ * Because scales are powers of two, the codes of an open block can take a
+ * larger exponent later without a second rounding, except in E4M3's
+ * subnormals (below 2^-6 * 2^e).  The two NaN codes are not part of the
+ * format: slots that some query sees must not hold them, other slots may.
+ * ------------------------------------------------------------------------- */
+typedef enum { CSA_ROPE_INTERLEAVED = 0, CSA_ROPE_HALF = 1 } csa_rope_layout;
+typedef enum { CSA_ROPE_NONE = 0, CSA_ROPE_LINEAR = 1, CSA_ROPE_PARTS = 2 } csa_rope_scaling;
+
+typedef struct {
+  int d;          /* head width */
+  int rope_dims;  /* rotated dims, even, 0 .. d */
+  int rope_off;   /* the first of them: dims rope_off .. rope_off+rope_dims-1 turn */
+  int layout;     /* csa_rope_layout: pair p is dims (2p, 2p+1), or
+                     (p, p + rope_dims/2), of the rotated ones */
+  int scaling;    /* csa_rope_scaling of the angles theta_p = base^(-2p/rope_dims):
+                     NONE; LINEAR: theta_p / factor; PARTS: with r = orig_len *
+                     theta_p / (2 pi) turns over the trained length and gamma =
+                     clamp((r - slow) / (fast - slow), 0, 1),
+                     theta_p * (gamma + (1 - gamma) / factor) */
+  float base;
+  float factor;   /* LINEAR, PARTS: > 0 */
+  float orig_len; /* PARTS: > 0 */
+  float fast, slow; /* PARTS: fast > slow */
+  float mscale;   /* multiplies the rotated dims (1: none) */
+} csa_rope;
+
+typedef struct {
+  int n_q;        /* query heads; query heads h n_q/n_kv .. read KV head h */
+  int n_kv;       /* KV heads, n_q % n_kv == 0 */
+  int d;          /* head width: 64, 128 or 256 */
+  int block;      /* slots that share an exponent: 16, 32, 64 or 128 */
+  int N;          /* slots per sequence and KV head, a multiple of block */
+  int act;        /* csa_dtype of q, k, v and out: CSA_F32 or CSA_BF16 */
+} csa_kv8_params;
+
+/* csa_rope_freqs: the table csa_qk_norm_rope reads, turns[p] = theta_p /
+ * (2 pi) after scaling (turns per token, fp64), rope_dims/2 entries in
+ * caller-owned device memory.  Computed once per model. */
+csa_status csa_rope_freqs(const csa_rope* r, double* turns, csa_stream_t stream);
+
+/* csa_qk_norm_rope: per head x <- gain * x / sqrt(mean(x^2) + eps) (skipped
+ * when norm = 0), then each pair (a, b) of the rotated dims turns by
+ * pos * theta_p: (a cos - b sin, a sin + b cos) * mscale; other dims keep
+ * their normalised value.  Queries and keys in one pass, computed in fp32
+ * (angles in fp64, so any int32 position keeps its accuracy) and rounded
+ * once.
+ *   pos     [R] int32            token positions (negative ones turn back)
+ *   q       [R][n_q][d]          act dtype, rows q_stride elements apart
+ *   k       [R][n_kv][d]         act dtype, rows k_stride apart; n_kv = 0 and
+ *                                NULL: queries only
+ *   q_gain, k_gain [d] fp32      NULL: unit gain
+ *   q_out, k_out                 as q and k, with their own row strides; may
+ *                                be q and k themselves (same stride)
+ * Row strides may exceed the row (views of one fused projection).  d % 8 ==
+ * 0, d <= 512; pointers and row strides multiples of 16 bytes.  R = 0 is a
+ * call that does nothing. */
+csa_status csa_qk_norm_rope(const csa_rope* r, int R, int n_q, int n_kv, int act, int norm,
+                            float eps, const double* turns, const int32_t* pos, const void* q,
+                            int64_t q_stride, const float* q_gain, const void* k,
+                            int64_t k_stride, const float* k_gain, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            csa_stream_t stream);
+
+/* csa_kv8_append: writes new tokens into the cache.  Token t of sequence b
+ * (t < n_new[b]) goes to slot n_old[b] + t of every KV head.  A block whose
+ * first slot is written starts afresh (its codes and exponent need no
+ * initialisation); in a block that already holds slots below n_old[b] the
+ * exponent never falls, and where it grows the earlier codes are rescaled.
+ * Nothing else of the cache is written.
+ *   k, v    [B][T][n_kv][d]      act dtype, tokens k_stride / v_stride
+ *                                elements apart (a token's heads contiguous)
+ *   n_old   [B] int32            slots in use before the call
+ *   n_new   [B] int32            tokens of each sequence, <= T (NULL: all T)
+ * Tokens beyond slot N are skipped and raise CSA_DEV_BAD_INDEX, as does an
+ * n_old outside [0, N] (its sequence is skipped) or an n_new outside [0, T]
+ * (clamped). */
+csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* n_old,
+                          const int32_t* n_new, void* kc, uint8_t* k_exp, void* vc,
+                          uint8_t* v_exp, csa_stream_t stream);
+
+/* csa_kv8_attend: softmax attention of each query head over the first
+ * n_vis[r] slots of its sequence and KV head; logits = scale * q . key, and
+ * with sink != NULL the denominator also holds exp(sink_h) (the sink logit is
+ * not scaled).  A row with n_vis <= 0 gives zeros.  Softmax statistics and
+ * sums in fp32.
+ *   q       [B*Q][n_q][d]        act dtype
+ *   n_vis   [B*Q] int32          slots each query sees (above N: clamped,
+ *                                CSA_DEV_BAD_INDEX)
+ *   sink    [n_q] fp32 or NULL
+ *   out     [B*Q][n_q][d]        act dtype
+ *   acc     [B][n_kv][N/block] fp32 or NULL: attention weight by block,
+ *           acc = decay * acc + the weights that the call's queries and the
+ *           KV head's query heads put on the block's slots (decay = 0: the
+ *           old value is not read); blocks no query of the sequence sees are
+ *           left as they are
+ *   workspace / ws_bytes         >= csa_kv8_attend_workspace_bytes(with_acc =
+ *           acc != NULL).  Calls that may run at the same time need their
+ *           own; nothing in it has to be kept between calls.
+ * Results do not depend on timing: a repeated call gives the same bits. */
+size_t csa_kv8_attend_workspace_bytes(const csa_kv8_params* p, int B, int Q, int with_acc);
+csa_status csa_kv8_attend(const csa_kv8_params* p, int B, int Q, float scale, const void* q,
+                          const int32_t* n_vis, const void* kc, const uint8_t* k_exp,
+                          const void* vc, const uint8_t* v_exp, const float* sink, void* out,
+                          float* acc, float decay, void* workspace, size_t ws_bytes,
+                          csa_stream_t stream);
+
+/* csa_kv8_evict: cuts every sequence that uses more than `keep` blocks (of
+ * nb = ceil(n_tok[b] / block)) down to `keep`, for each KV head on its own:
+ * the last `recent` blocks stay, and of the others the keep - recent with the
+ * largest acc (ties: the lower index; NaN counts as the least).  In place,
+ * moving as little as possible: a kept block below slot block keep-1 stays
+ * where it is; the free ones there take the kept blocks from keep-1 on in
+ * ascending order; block keep-1 becomes the old last block, the one that may
+ * be open.  (Attention over the cache does not depend on the order of slots;
+ * keys are stored rotated.)
+ *   acc     [B][n_kv][N/block] fp32   n_tok [B] int32, in [0, N] (else
+ *           CSA_DEV_BAD_INDEX, and the sequence is left as it is)
+ *   kept    [B][n_kv][keep] int32     out: the block each block now holds was
+ *           (-1: none)
+ *   acc_out [B][n_kv][N/block] fp32   out: acc of the blocks now held, 0
+ *           beyond; may be acc itself
+ *   n_tok_out [B] int32               out: slots in use; may be n_tok itself
+ * 1 <= recent <= keep <= N/block <= 262144. */
+csa_status csa_kv8_evict(const csa_kv8_params* p, int B, int keep, int recent, const float* acc,
+                         const int32_t* n_tok, void* kc, uint8_t* k_exp, void* vc,
+                         uint8_t* v_exp, int32_t* kept, float* acc_out, int32_t* n_tok_out,
+                         csa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status and diagnostics.

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa.so")
 
 CSA_F32, CSA_BF16, CSA_KV_FP8MIX = 0, 1, 2
 _DT = {"f32": CSA_F32, "bf16": CSA_BF16, "fp8mix": CSA_KV_FP8MIX}
-DEV_BAD_INDEX, DEV_BAD_WINDOW, DEV_TIMEOUT, DEV_RANGE = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_INDEX, DEV_BAD_WINDOW, DEV_TIMEOUT, DEV_RANGE, DEV_NAN = 0x1, 0x2, 0x4, 0x8, 0x10
 
 
 class CsaError(RuntimeError):
@@ -86,6 +86,17 @@ _SIGS = {
                              _vp, _vp, _sz, _vp]),
     "hca_attend": (C.c_int, [_P, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp,
                              _vp, _vp, _sz, _vp]),
+    "csa_rope_freqs": (C.c_int, [_vp, _vp, _vp]),
+    "csa_qk_norm_rope": (C.c_int, [_vp, _i, _i, _i, _i, _i, C.c_float, _vp, _vp, _vp, C.c_int64,
+                                   _vp, _vp, C.c_int64, _vp, _vp, C.c_int64, _vp, C.c_int64,
+                                   _vp]),
+    "csa_kv8_append": (C.c_int, [_vp, _i, _i, _vp, C.c_int64, _vp, C.c_int64, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _vp]),
+    "csa_kv8_attend_workspace_bytes": (_sz, [_vp, _i, _i, _i]),
+    "csa_kv8_attend": (C.c_int, [_vp, _i, _i, C.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, C.c_float, _vp, _sz, _vp]),
+    "csa_kv8_evict": (C.c_int, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp]),
 }
 
 
@@ -537,3 +548,211 @@ def hca_attend(p: CsaParams, q_pos, q, ckv, ckv_scale, win, win_scale, win_pos0,
                           _p(win), _p(win_scale), W, _p(win_pos0), _p(sink), _p(out),
                           _p(ws), wsb, _stream(stream))
     _check("hca_attend", st)
+
+
+# ------------------------------------------- uncompressed layers: 8-bit KV --
+ROPE_LAYOUT = {"interleaved": 0, "half": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "parts": 2}
+
+
+class CsaRope(C.Structure):
+    _fields_ = [("d", C.c_int), ("rope_dims", C.c_int), ("rope_off", C.c_int),
+                ("layout", C.c_int), ("scaling", C.c_int), ("base", C.c_float),
+                ("factor", C.c_float), ("orig_len", C.c_float), ("fast", C.c_float),
+                ("slow", C.c_float), ("mscale", C.c_float)]
+
+
+class CsaKv8Params(C.Structure):
+    _fields_ = [("n_q", C.c_int), ("n_kv", C.c_int), ("d", C.c_int), ("block", C.c_int),
+                ("N", C.c_int), ("act", C.c_int)]
+
+
+def rope_params(d, rope_dims, rope_off=None, layout="interleaved", base=10000.0, scaling="none",
+                factor=1.0, orig_len=0.0, fast=32.0, slow=1.0, mscale=1.0) -> CsaRope:
+    """csa_rope: the last rope_dims of d by default, as everywhere in the library."""
+    return CsaRope(d, rope_dims, d - rope_dims if rope_off is None else rope_off,
+                   ROPE_LAYOUT[layout], ROPE_SCALING[scaling], base, factor, orig_len, fast, slow,
+                   mscale)
+
+
+def kv8_params(n_q, n_kv, d, block, N, act) -> CsaKv8Params:
+    """csa_kv8_params; act is "bf16" or "f32"."""
+    if act not in ("bf16", "f32"):
+        raise ValueError(f"act: 'bf16' or 'f32' expected, got {act!r}")
+    return CsaKv8Params(n_q, n_kv, d, block, N, _DT[act])
+
+
+def _dense(t, dtype, shape, what, dev):
+    """A contiguous device tensor of that dtype, shape and device; its address."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{what}: on {t.device}, the call is on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous tensor expected")
+    return t.data_ptr()
+
+
+def _token_stride(t, dtype, what, dev):
+    """Elements between the tokens of t [R][heads][d] whose rows may be part
+    of wider ones; a token's heads are contiguous."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{what}: on {t.device}, the call is on {dev}")
+    R, n, d = t.shape
+    sr, sn, sd = t.stride()
+    if (sd != 1 and d > 1) or (sn != d and n > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return sr if R > 1 else n * d
+
+
+def _cuda_dev(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: device tensor expected")
+    return t.device
+
+
+def _launch(name, dev, stream, *args):
+    """Call the library on the tensors' device and the given or current
+    stream of that device."""
+    fn = getattr(_lib or lib(), name)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != 0:
+        _check(name, st)
+
+
+def csa_rope_freqs(rope: CsaRope, device="cuda", stream=None) -> torch.Tensor:
+    """The fp64 table [rope_dims/2] of turns per token that csa_qk_norm_rope reads."""
+    turns = torch.empty(rope.rope_dims // 2, dtype=torch.float64, device=device)
+    if stream is not None:
+        turns.record_stream(stream)
+    _launch("csa_rope_freqs", turns.device, stream, C.byref(rope), turns.data_ptr() or None)
+    return turns
+
+
+def csa_qk_norm_rope(rope: CsaRope, turns, pos, q, k, q_out, k_out, q_gain=None, k_gain=None,
+                     eps=1e-6, norm=True, stream=None):
+    """q [R][n_q][d] and k [R][n_kv][d] (k and k_out None: queries only) at
+    positions pos [R] -> q_out, k_out of the same shapes (q and k themselves
+    for in place).  Tokens may be rows of a wider tensor."""
+    dev = _cuda_dev(q, "q")
+    act = q.dtype
+    if act is not torch.bfloat16 and act is not torch.float32:
+        raise ValueError(f"q: torch.bfloat16 or torch.float32 expected, got {act}")
+    R, n_q, d = q.shape
+    if d != rope.d:
+        raise ValueError(f"q: heads of {rope.d} expected, got {d}")
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out: shape {tuple(q.shape)} expected, got {tuple(q_out.shape)}")
+    qs, qos = _token_stride(q, act, "q", dev), _token_stride(q_out, act, "q_out", dev)
+    n_kv, ks, kos, kp, kop = 0, 0, 0, None, None
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither")
+    if k is not None:
+        n_kv = k.shape[1]
+        if k.shape != (R, n_kv, d) or k_out.shape != k.shape:
+            raise ValueError(f"k, k_out: [{R}][n_kv][{d}] expected, got {tuple(k.shape)} and "
+                             f"{tuple(k_out.shape)}")
+        ks, kos = _token_stride(k, act, "k", dev), _token_stride(k_out, act, "k_out", dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    if (q.data_ptr() == q_out.data_ptr() and qs != qos) or (kp is not None and kp == kop and ks != kos):
+        raise ValueError("in place: the row strides must be the same")
+    _launch("csa_qk_norm_rope", dev, stream, C.byref(rope), R, n_q, n_kv,
+            CSA_F32 if act is torch.float32 else CSA_BF16, 1 if norm else 0, eps,
+            _dense(turns, torch.float64, (rope.rope_dims // 2,), "turns", dev),
+            _dense(pos, torch.int32, (R,), "pos", dev), q.data_ptr(), qs,
+            None if q_gain is None else _dense(q_gain, torch.float32, (d,), "q_gain", dev), kp, ks,
+            None if k_gain is None else _dense(k_gain, torch.float32, (d,), "k_gain", dev),
+            q_out.data_ptr(), qos, kop, kos)
+
+
+def _kv8_cache(p: CsaKv8Params, kc, k_exp, vc, v_exp, dev):
+    """Addresses of the four tensors of an 8-bit cache, and its sequences."""
+    B = kc.shape[0]
+    codes, exps = (B, p.n_kv, p.N, p.d), (B, p.n_kv, p.N // max(p.block, 1))
+    return B, (_dense(kc, torch.uint8, codes, "kc", dev), _dense(k_exp, torch.uint8, exps, "k_exp", dev),
+               _dense(vc, torch.uint8, codes, "vc", dev), _dense(v_exp, torch.uint8, exps, "v_exp", dev))
+
+
+def csa_kv8_append(p: CsaKv8Params, k, v, n_old, kc, k_exp, vc, v_exp, n_new=None, stream=None):
+    """k, v [B][T][n_kv][d] into the cache kc, vc [B][n_kv][N][d] (uint8 E4M3
+    codes) and k_exp, v_exp [B][n_kv][N/block] (uint8) behind the n_old [B]
+    slots in use; n_new [B]: tokens of each sequence (None: T)."""
+    dev = _cuda_dev(k, "k")
+    act = torch.float32 if p.act == CSA_F32 else torch.bfloat16
+    B, cache = _kv8_cache(p, kc, k_exp, vc, v_exp, dev)
+    T = k.shape[1]
+    strides = []
+    for t, what in ((k, "k"), (v, "v")):
+        if t.shape != (B, T, p.n_kv, p.d):
+            raise ValueError(f"{what}: [{B}][{T}][{p.n_kv}][{p.d}] expected, got {tuple(t.shape)}")
+        s = t.stride()
+        if B > 1 and T > 1 and s[0] != T * s[1]:
+            raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
+        strides.append(_token_stride(t[0] if T > 1 else t[:, 0] if T == 1 else t.new_empty(0, p.n_kv, p.d),
+                                     act, what, dev))
+    _launch("csa_kv8_append", dev, stream, C.byref(p), B, T, k.data_ptr(), strides[0], v.data_ptr(),
+            strides[1], _dense(n_old, torch.int32, (B,), "n_old", dev),
+            None if n_new is None else _dense(n_new, torch.int32, (B,), "n_new", dev), *cache)
+
+
+def kv8_attend_workspace_bytes(p: CsaKv8Params, B, Q, with_acc=False) -> int:
+    return lib().csa_kv8_attend_workspace_bytes(C.byref(p), B, Q, 1 if with_acc else 0)
+
+
+def csa_kv8_attend(p: CsaKv8Params, q, n_vis, kc, k_exp, vc, v_exp, out, sink=None, scale=None,
+                   acc=None, decay=1.0, workspace=None, stream=None):
+    """q [B*Q][n_q][d] over the first n_vis [B*Q] slots of the cache -> out
+    [B*Q][n_q][d].  scale: of the logits (None: d^-0.5); sink [n_q] fp32;
+    acc [B][n_kv][N/block] fp32: acc = decay * acc + attention weight."""
+    dev = _cuda_dev(q, "q")
+    act = torch.float32 if p.act == CSA_F32 else torch.bfloat16
+    B, cache = _kv8_cache(p, kc, k_exp, vc, v_exp, dev)
+    R = q.shape[0]
+    Q = _per_seq(R, B, "q")
+    shape = (R, p.n_q, p.d)
+    qp, op = _dense(q, act, shape, "q", dev), _dense(out, act, shape, "out", dev)
+    ap = None if acc is None else _dense(acc, torch.float32, (B, p.n_kv, p.N // max(p.block, 1)), "acc", dev)
+    need = lib().csa_kv8_attend_workspace_bytes(C.byref(p), B, Q, 0 if acc is None else 1)
+    wp, wb = None, 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous tensor on {dev} expected")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("csa_kv8_attend", dev, stream, C.byref(p), B, Q, p.d ** -0.5 if scale is None else scale,
+            qp, _dense(n_vis, torch.int32, (R,), "n_vis", dev), *cache,
+            None if sink is None else _dense(sink, torch.float32, (p.n_q,), "sink", dev), op, ap,
+            decay, wp, wb)
+
+
+def csa_kv8_evict(p: CsaKv8Params, keep, recent, acc, n_tok, kc, k_exp, vc, v_exp, kept, acc_out,
+                  n_tok_out, stream=None):
+    """Cut sequences of more than `keep` blocks down to keep, by acc
+    [B][n_kv][N/block]; kept [B][n_kv][keep] int32, acc_out as acc and
+    n_tok_out [B] as n_tok (both may be the inputs themselves)."""
+    dev = _cuda_dev(acc, "acc")
+    B, cache = _kv8_cache(p, kc, k_exp, vc, v_exp, dev)
+    shape = (B, p.n_kv, p.N // max(p.block, 1))
+    _launch("csa_kv8_evict", dev, stream, C.byref(p), B, keep, recent,
+            _dense(acc, torch.float32, shape, "acc", dev),
+            _dense(n_tok, torch.int32, (B,), "n_tok", dev), *cache,
+            _dense(kept, torch.int32, (B, p.n_kv, keep), "kept", dev),
+            _dense(acc_out, torch.float32, shape, "acc_out", dev),
+            _dense(n_tok_out, torch.int32, (B,), "n_tok_out", dev))

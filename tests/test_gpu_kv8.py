@@ -1,0 +1,476 @@
+"""The 8-bit KV cache path against its fp64 oracle (oracle/kv8.py): norm and
+rotation, append, attention with accumulated weights, eviction, and a run of
+them together.
+
+Tolerances.  U = 2^-24 is half a step of fp32 relative to the value, 2^-8 of
+bf16, 2^-12 of fp16 (the type the attention's probabilities are rounded to).
+* norm + rotation: the gain of an element carries the rounded sum of squares
+  (at most 16 sequential adds and 5 of a tree, halved by the root: 11 U),
+  root, divide and two products (4 U); the rotation the angle's rounding
+  (half turns in fp32: pi U), sine and cosine (2 ulp: 4 U), mscale and two
+  products and a sum (4 U): at most 32 U (|a| + |b|), then the output's
+  rounding.
+* attention: logits are sums of d products accumulated in fp32 (tensor cores
+  may truncate: a full step 2 U each), with q held to 2^-22 at least; a logit
+  is off by at most eps = (2 d + 16) U * load + 8 U * |logit range| where
+  load = max scale sum |q||k|, so weights by 2 eps; p is rounded to fp16
+  (2^-11 with the block's power of two, bf16 activations) or to two fp16
+  terms (2^-22, fp32 activations) and summed over n / 16 steps of truncating
+  fp32.  The output is off by at most (2 eps + p rounding + (n / 8 + 16) U)
+  times sum p |v|, then its own rounding.
+* append and eviction: exact.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8
+from long_context_sparse_09_b200 import binding as bd
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {"f32": U, "bf16": 2.0 ** -8}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(autouse=True)
+def _clean_status(cuda_ok):
+    bd.device_status()
+    yield
+    torch.cuda.synchronize()
+    assert bd.device_status() == 0
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def within(got, ref, tol, what):
+    assert np.all(np.isfinite(got)), what
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst by " \
+        f"{(np.abs(got - ref) / np.maximum(tol, 1e-300)).max():.3g} tolerances"
+
+
+# ------------------------------------------------------- norm and rotation --
+NORM = [
+    # act, R, n_q, n_kv, d, rope_dims, rope_off, layout, scaling, norm, gain
+    ("bf16", 1, 64, 8, 128, 128, 0, "half", "parts", True, True),
+    ("bf16", 7, 5, 1, 64, 32, 32, "interleaved", "none", True, False),
+    ("f32", 33, 3, 3, 96, 96, 0, "half", "linear", True, True),
+    ("f32", 300, 4, 0, 512, 64, 448, "interleaved", "parts", True, True),
+    ("bf16", 65, 9, 2, 256, 34, 5, "half", "none", True, True),
+    ("bf16", 3, 2, 1, 8, 8, 0, "interleaved", "none", False, False),
+    ("f32", 2, 17, 4, 40, 2, 38, "half", "none", False, False),
+    ("bf16", 4, 3, 2, 128, 0, 0, "half", "none", True, True),
+    ("bf16", 5, 2, 1, 264, 264, 0, "interleaved", "linear", True, True),
+]
+SCALE = dict(factor=8.0, orig_len=4096.0)
+
+
+def norm_rope_case(act, R, n_q, n_kv, d, D, off, layout, scaling, norm, gain, seed=0, wide=0):
+    g = torch.Generator().manual_seed(seed + R * 31 + d)
+    row = (n_q + n_kv) * d + wide
+    x = (torch.randn(R, row, generator=g) * 2).to(DT[act]).to(DEV)
+    q, k = x[:, :n_q * d].view(R, n_q, d), x[:, n_q * d:(n_q + n_kv) * d].view(R, n_kv, d)
+    pos = torch.randint(-5, 1 << 20, (R,), generator=g, dtype=torch.int32)
+    pos[0] = (1 << 31) - 1
+    gains = [torch.randn(d, generator=g) if gain else None for _ in range(2)]
+    mscale = 1.2 if scaling == "parts" else 1.0
+    rope = bd.rope_params(d, D, off, layout, scaling=scaling, mscale=mscale, **SCALE)
+    kw = SCALE if scaling != "none" else {}
+    return rope, q, k, pos, gains, mscale, kv8.turns(D, scaling=scaling, **kw)
+
+
+@pytest.mark.parametrize("case", NORM, ids=[f"{c[0]}-R{c[1]}-d{c[4]}-{c[5]}at{c[6]}-{c[7]}" for c in NORM])
+@pytest.mark.parametrize("wide", [0, 64])
+def test_norm_rope(case, wide):
+    act, R, n_q, n_kv, d, D, off, layout, scaling, norm, gain = case
+    rope, q, k, pos, gains, mscale, t = norm_rope_case(*case, wide=wide)
+    turns = bd.csa_rope_freqs(rope)
+    # pow to 2 ulp of fp64, a few more operations
+    assert np.all(np.abs(np64(turns) - t) <= 16 * 2.0 ** -53 * t)
+    q_ref, k_ref = np64(q), np64(k)
+    q_out = torch.empty(R, n_q, d, dtype=q.dtype, device=DEV)
+    k_out = torch.empty(R, n_kv, d, dtype=q.dtype, device=DEV) if n_kv else None
+    dev = [None if x is None else x.to(DEV) for x in gains]
+    for call in range(2):   # into new tensors, then in place
+        o = (q_out, k_out) if call == 0 else (q, k if n_kv else None)
+        bd.csa_qk_norm_rope(rope, turns, pos.to(DEV), q, k if n_kv else None, *o, q_gain=dev[0],
+                            k_gain=dev[1], norm=norm)
+        for got, x, gn, what in ((o[0], q_ref, gains[0], "q"), (o[1], k_ref, gains[1], "k")):
+            if got is None:
+                continue
+            # turns may differ by 16 half steps of fp64: at 2^31 tokens that is 2^31 * t * 2^-49 turns
+            drift = 2 * np.pi * 2.0 ** 31 * 2.0 ** -49 * (t.max() if len(t) else 0.0)
+            ref, mag = kv8.norm_rope(x, pos.numpy(), t, off, layout, gn, norm=norm, mscale=mscale)
+            within(np64(got), ref, HALF[act] * np.abs(ref) + (32 * U + drift) * mag, f"{what} call {call}")
+
+
+def test_norm_rope_of_nothing_and_of_zeros():
+    rope = bd.rope_params(64, 64)
+    turns = bd.csa_rope_freqs(rope)
+    e = torch.empty(0, 4, 64, device=DEV)
+    bd.csa_qk_norm_rope(rope, turns, torch.empty(0, dtype=torch.int32, device=DEV), e, None, e, None)
+    z = torch.zeros(3, 4, 64, device=DEV)
+    out = torch.full_like(z, float("nan"))
+    bd.csa_qk_norm_rope(rope, turns, torch.arange(3, dtype=torch.int32, device=DEV), z, None, out, None)
+    assert torch.equal(out, z)
+
+
+# ------------------------------------------------------------------ append --
+APPEND = [
+    # act, B, T, H, d, block, N, n_old, n_new (None: T)
+    ("bf16", 1, 1, 1, 64, 16, 16, [0], None),
+    ("bf16", 3, 1, 2, 128, 64, 256, [63, 64, 255], None),
+    ("bf16", 2, 100, 3, 64, 32, 192, [5, 31], [100, 37]),
+    ("f32", 4, 33, 2, 128, 16, 128, [0, 95, 17, 40], [33, 33, 0, 1]),
+    ("f32", 1, 300, 1, 256, 128, 384, [77], None),
+    ("bf16", 2, 129, 1, 256, 128, 384, [127, 255], None),
+    ("f32", 1, 0, 2, 64, 16, 32, [3], None),
+]
+
+
+def random_cache(B, H, N, d, block, seed, lo=112, hi=126):
+    g = torch.Generator().manual_seed(seed)
+    c = torch.randint(0, 256, (2, B, H, N, d), generator=g, dtype=torch.uint8)
+    c[(c & 0x7f) == 0x7f] = 0x11
+    return c, torch.randint(lo, hi, (2, B, H, N // block), generator=g, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("case", APPEND, ids=[f"{c[0]}-B{c[1]}-T{c[2]}-d{c[4]}-blk{c[5]}" for c in APPEND])
+@pytest.mark.parametrize("spread", [False, True])
+def test_append_is_exact(case, spread):
+    act, B, T, H, d, block, N, n_old, n_new = case
+    g = torch.Generator().manual_seed(T * 7 + d)
+    x = torch.randn(2, B, T, H, d, generator=g) * torch.exp(3 * torch.randn(2, B, T, 1, 1, generator=g))
+    if x.numel():   # values whose scaling meets zeros, subnormals, ends of the range
+        flat = x.view(-1)
+        special = [0.0, -0.0, 1e-40, 3e38, -3e38, float("inf"), float("-inf"), 448.0, 1.75]
+        at = torch.randint(0, flat.numel(), (len(special),), generator=g)
+        flat[at] = torch.tensor(special) if T > 2 else torch.tensor([0.0, 1.75, -0.0] * 3)
+    x = x.to(DT[act])
+    p = bd.kv8_params(H, H, d, block, N, act)
+    codes, exps = random_cache(B, H, N, d, block, 5)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    xd = x.to(DEV)
+    if spread:   # tokens as rows of a wider tensor
+        wide = torch.zeros(2, B, T, 2 * H, d, dtype=x.dtype, device=DEV)
+        wide[:, :, :, :H] = xd
+        xd = wide[:, :, :, :H]
+    new = None if n_new is None else torch.tensor(n_new, dtype=torch.int32, device=DEV)
+    bd.csa_kv8_append(p, xd[0], xd[1], torch.tensor(n_old, dtype=torch.int32, device=DEV), dc[0], de[0],
+                      dc[1], de[1], n_new=new)
+    assert bd.device_status() == 0
+    for i in range(2):
+        c, e = codes[i].numpy().copy(), exps[i].numpy().copy()
+        kv8.append(x[i].double().numpy(), n_old, n_new or [T] * B, c, e, block)
+        assert np.array_equal(de[i].cpu().numpy(), e), f"exponents of {'kv'[i]}"
+        got = dc[i].cpu().numpy()
+        assert np.array_equal(kv8._TAB[got], kv8._TAB[c]), f"codes of {'kv'[i]}"
+
+
+def test_append_token_by_token_from_uninitialised_blocks():
+    """Blocks start afresh: what the memory held before does not matter."""
+    B, T, H, d, block, N = 2, 40, 2, 64, 16, 48
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(2, B, T, H, d, generator=g) * torch.exp2(torch.arange(T) / 4.0)[:, None, None]
+    p = bd.kv8_params(H, H, d, block, N, "f32")
+    dc = torch.full((2, B, H, N, d), 255, dtype=torch.uint8, device=DEV)
+    de = torch.full((2, B, H, N // block), 255, dtype=torch.uint8, device=DEV)
+    c, e = np.zeros((2, B, H, N, d), np.uint8), np.zeros((2, B, H, N // block), np.uint8)
+    for t in range(T):
+        xt = x[:, :, t:t + 1].to(DEV)
+        bd.csa_kv8_append(p, xt[0], xt[1], torch.full((B,), t, dtype=torch.int32, device=DEV), dc[0], de[0],
+                          dc[1], de[1])
+        for i in range(2):
+            kv8.append(x[i, :, t:t + 1].double().numpy(), [t] * B, [1] * B, c[i], e[i], block)
+    nb = -(-T // block)
+    assert np.array_equal(de.cpu().numpy()[..., :nb], e[..., :nb])
+    assert np.array_equal(dc.cpu().numpy()[..., :T, :], c[..., :T, :])
+    assert (dc[..., T:, :] == 255).all() and (de[..., nb:] == 255).all()
+
+
+def test_append_reports_bad_lengths_and_nan():
+    B, T, H, d, block, N = 4, 8, 1, 64, 16, 32
+    p = bd.kv8_params(H, H, d, block, N, "f32")
+    x = torch.randn(B, T, H, d, device=DEV)
+    full = torch.full((B, H, N, d), 7, dtype=torch.uint8, device=DEV)
+    kc, vc = full.clone(), full.clone()
+    ke, ve = (torch.full((B, H, N // block), 120, dtype=torch.uint8, device=DEV) for _ in range(2))
+    old = torch.tensor([-1, 33, 28, 0], dtype=torch.int32, device=DEV)
+    new = torch.tensor([8, 8, 8, 9], dtype=torch.int32, device=DEV)
+    bd.csa_kv8_append(p, x, x, old, kc, ke, vc, ve, n_new=new)
+    assert bd.device_status() == bd.DEV_BAD_INDEX
+    assert torch.equal(kc[:2], full[:2])            # skipped
+    assert torch.equal(kc[2, :, :16], full[2, :, :16]) and not torch.equal(kc[2, :, 28:], full[2, :, 28:])
+    assert torch.equal(kc[3, :, 8:], full[3, :, 8:])  # n_new above T: T tokens
+    x[0, 3, 0, 5] = float("nan")
+    bd.csa_kv8_append(p, x, x, torch.zeros_like(old), kc, ke, vc, ve)
+    assert bd.device_status() == bd.DEV_NAN
+    assert kc[0, 0, 3, 5] == 0 and ke[0, 0, 0] < 130
+
+
+# ------------------------------------------------------------------ attend --
+ATTEND = [
+    # act, B, Q, n_q, n_kv, d, block, N, n_vis, sink, acc
+    ("bf16", 1, 1, 1, 1, 64, 16, 16, [1], False, False),
+    ("bf16", 2, 1, 8, 2, 128, 64, 192, [0, 65], True, True),
+    ("f32", 2, 1, 6, 6, 64, 32, 96, [96, 33], False, True),
+    ("bf16", 3, 1, 14, 2, 128, 16, 2048, [2048, 1, 1337], False, True),
+    ("f32", 1, 3, 12, 3, 256, 128, 640, [538, 539, 540], True, False),
+    ("bf16", 1, 5, 32, 1, 64, 32, 1024, [997, 998, 999, 1000, 1001], False, True),
+    ("bf16", 2, 4, 16, 16, 256, 64, 320, [0, 1, 0, 320, 64, 63, 128, 7], True, True),
+    ("bf16", 1, 70, 8, 2, 128, 64, 256, list(range(100, 170)), False, False),
+    ("bf16", 2, 33, 6, 3, 64, 16, 128, list(range(-2, 31)) + list(range(96, 129)), True, True),
+    ("f32", 1, 40, 4, 4, 128, 32, 160, list(range(1, 160, 4)), True, True),
+    ("bf16", 1, 150, 8, 1, 128, 128, 512, list(range(0, 300, 2)), True, False),
+    ("bf16", 1, 300, 2, 1, 64, 64, 384, list(range(1, 301)), False, True),
+]
+
+
+def attend_tol(act, d, n, ref, mag, load, scale_range):
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * scale_range
+    p_round = 2.0 ** -11 if act == "bf16" else 2.0 ** -22
+    return HALF[act] * np.abs(ref) + (2 * eps + p_round + (n / 8 + 16) * U) * mag
+
+
+def attend_inputs(case, seed, garbage=True):
+    act, B, Q, n_q, n_kv, d, block, N, n_vis, sink, acc = case
+    g = torch.Generator().manual_seed(seed)
+    codes, exps = random_cache(B, n_kv, N, d, block, seed, 115, 121)
+    codes = (torch.randn(codes.shape, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = (torch.randn(B * Q, n_q, d, generator=g) * 2).to(DT[act])
+    vis = torch.tensor(n_vis, dtype=torch.int32)
+    clean = codes.clone()
+    if garbage:   # NaN codes and wild exponents in slots that nothing sees
+        for b in range(B):
+            top = max(0, int(vis[b * Q:(b + 1) * Q].max()))
+            codes[:, b, :, top:] = 0x7f
+            exps[:, b, :, -(-top // block):] = 255
+    z = torch.randn(n_q, generator=g) * 3 if sink else None
+    w = torch.rand(B, n_kv, N // block, generator=g) if acc else None
+    return clean, codes, exps, q, vis, z, w
+
+
+def check_attend(case, seed, decay=1.0):
+    act, B, Q, n_q, n_kv, d, block, N, n_vis, sink, acc = case
+    clean, codes, exps, q, vis, z, w = attend_inputs(case, seed)
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    out = torch.full((B * Q, n_q, d), float("nan"), dtype=DT[act], device=DEV)
+    dw = None if w is None else w.to(DEV)
+    if decay == 0.0 and dw is not None:
+        dw.fill_(float("nan"))
+    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out,
+                      sink=None if z is None else z.to(DEV), acc=dw, decay=decay)
+    exps_ref = np.where(exps.numpy() == 255, 127, exps.numpy())
+    K, V = (kv8.values(clean[i].numpy(), exps_ref[i], block) for i in range(2))
+    scale = d ** -0.5
+    ref, wref, mag, load = kv8.attend(q.double().numpy(), n_vis, K, V, block, scale,
+                                      None if z is None else z.double().numpy())
+    rng = float(load.max(initial=0.0))
+    within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, rng) + 1e-30, "out")
+    if dw is not None:
+        # every weight by 2 eps and the sums over a block's slots and the rows
+        eps = (2 * d + 16) * U * load.max(initial=0.0) + 8 * U * rng
+        got = np64(dw)
+        for b in range(B):
+            top = -(-max(0, max(n_vis[b * Q:(b + 1) * Q])) // block)
+            old = decay * w[b, :, :top].double().numpy() if decay else 0.0
+            within(got[b, :, :top], old + wref[b, :, :top],
+                   (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * wref[b, :, :top] + 2 * U * old + 1e-30, "acc")
+            rest = got[b, :, top:]   # blocks no query sees: untouched
+            assert np.isnan(rest).all() if decay == 0.0 else np.array_equal(rest, w[b, :, top:].double().numpy())
+    return out, dw
+
+
+IDS = [f"{c[0]}-B{c[1]}-Q{c[2]}-h{c[3]}of{c[4]}-d{c[5]}-blk{c[6]}" for c in ATTEND]
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=IDS)
+def test_attend(case):
+    check_attend(case, 11)
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.75])
+def test_attend_decay(decay):
+    check_attend(ATTEND[3], 12, decay)
+    check_attend(ATTEND[8], 12, decay)
+
+
+def test_attend_is_repeatable_bit_for_bit():
+    case = ("bf16", 2, 1, 16, 2, 128, 64, 8192, [8000, 5000], True, True)
+    a, wa = check_attend(case, 13)
+    b, wb = check_attend(case, 13)
+    assert torch.equal(a, b) and torch.equal(wa, wb)
+
+
+@pytest.mark.parametrize("Q", [1, 2])
+def test_attend_extreme_values(Q):
+    """Query magnitudes far from 1, block exponents far apart, logits that
+    leave one slot, and a slot with a tiny value that takes all weight."""
+    B, n_q, n_kv, d, block, N = 1, 4, 2, 64, 16, 64
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "bf16")
+    codes, exps = random_cache(B, n_kv, N, d, block, 3, 118, 122)
+    for qmag, kexp, vexp in ((1e-30, 127 + 90, 127 - 100), (1e30, 127 - 100, 127 + 90), (1.0, 120, 127)):
+        e = exps.clone()
+        e[0] = kexp - 4
+        e[0, :, :, 1] = kexp
+        e[1] = vexp
+        e[1, :, :, 1] = vexp - 20
+        q = (torch.randn(B * Q, n_q, d, generator=torch.Generator().manual_seed(4)) * qmag).to(torch.bfloat16)
+        vis = [50] * Q
+        K, V = (kv8.values(codes[i].numpy(), e[i].numpy(), block) for i in range(2))
+        K[:, :, 50:] = V[:, :, 50:] = 0
+        qs = q.double().numpy()
+        scale = 2.0 / np.abs(np.einsum("rhd,hnd->rhn", qs, np.repeat(K[0], 2, 0))).std()
+        out = torch.empty(B * Q, n_q, d, dtype=torch.bfloat16, device=DEV)
+        dc, de = codes.to(DEV), e.to(DEV)
+        bd.csa_kv8_attend(p, q.to(DEV), torch.tensor(vis, dtype=torch.int32, device=DEV), dc[0], de[0], dc[1],
+                          de[1], out, scale=float(np.float32(scale)))
+        ref, _, mag, load = kv8.attend(qs, vis, K, V, block, float(np.float32(scale)))
+        rng = float(load.max())
+        within(np64(out), ref, attend_tol("bf16", d, N, ref, mag, load, rng), f"q {qmag}")
+
+
+def test_attend_clamps_and_reports_a_length_beyond_the_cache():
+    case = ("bf16", 2, 1, 4, 2, 64, 16, 64, [70, 64], False, False)
+    _, codes, exps, q, _, _, _ = attend_inputs(case, 1, garbage=False)
+    p = bd.kv8_params(4, 2, 64, 16, 64, "bf16")
+    dc, de, qd = codes.to(DEV), exps.to(DEV), q.to(DEV)
+    outs = []
+    for v in ([70, 64], [64, 64]):
+        outs.append(torch.empty_like(qd))
+        bd.csa_kv8_attend(p, qd, torch.tensor(v, dtype=torch.int32, device=DEV), dc[0], de[0], dc[1], de[1], outs[-1])
+        assert bd.device_status() == (bd.DEV_BAD_INDEX if v[0] == 70 else 0)
+    assert torch.equal(*outs)
+
+
+# ------------------------------------------------------------------- evict --
+EVICT = [
+    # B, H, d, block, N, n_tok, keep, recent
+    (1, 1, 64, 16, 16, [16], 1, 1),
+    (2, 2, 64, 16, 160, [153, 16], 1, 1),
+    (3, 2, 128, 64, 640, [640, 321, 0], 4, 2),
+    (2, 3, 64, 32, 3200, [3190, 1601], 50, 50),
+    (1, 2, 256, 16, 1024, [1009], 63, 3),
+    (2, 1, 64, 16, 40000, [39990, 20001], 700, 8),
+    (1, 1, 64, 128, 8192, [8191], 64, 1),
+]
+
+
+@pytest.mark.parametrize("case", EVICT, ids=[f"B{c[0]}-d{c[2]}-blk{c[3]}-N{c[4]}-keep{c[6]}" for c in EVICT])
+@pytest.mark.parametrize("kind", ["random", "ties", "odd"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_evict_is_exact(case, kind, inplace):
+    B, H, d, block, N, n_tok, keep, recent = case
+    NB = N // block
+    g = torch.Generator().manual_seed(NB + keep)
+    acc = torch.rand(B, H, NB, generator=g) ** 3
+    if kind == "ties":
+        acc = torch.randint(0, 3, (B, H, NB), generator=g).float()
+    elif kind == "odd":
+        acc = torch.randn(B, H, NB, generator=g)
+        acc[..., ::3] = float("nan")
+        acc[..., 1::5] = float("-inf")
+        acc[..., 2::7] = float("inf")
+        acc[..., 4::9] = -0.0
+    codes, exps = random_cache(B, H, N, d, block, NB)
+    p = bd.kv8_params(H, H, d, block, N, "bf16")
+    dc, de, da = codes.to(DEV), exps.to(DEV), acc.to(DEV)
+    dn = torch.tensor(n_tok, dtype=torch.int32, device=DEV)
+    ao, no = (da, dn) if inplace else (torch.full_like(da, 3.0), torch.full_like(dn, -5))
+    kept = torch.full((B, H, keep), -7, dtype=torch.int32, device=DEV)
+    bd.csa_kv8_evict(p, keep, recent, da, dn, dc[0], de[0], dc[1], de[1], kept, ao, no)
+    ref_kept, ref_acc, ref_n = kv8.evict(acc.numpy(), n_tok, keep, recent, block)
+    assert np.array_equal(kept.cpu().numpy(), ref_kept)
+    assert np.array_equal(ao.cpu().numpy(), ref_acc, equal_nan=True)
+    assert np.array_equal(no.cpu().numpy(), ref_n)
+    for i in range(2):
+        got = dc[i].cpu().view(B, H, NB, block * d)
+        was = codes[i].view(B, H, NB, block * d)
+        for b in range(B):
+            for h in range(H):
+                m = ref_kept[b, h][ref_kept[b, h] >= 0]
+                assert torch.equal(got[b, h, :len(m)], was[b, h][torch.from_numpy(m).long()])
+                assert torch.equal(got[b, h, keep:], was[b, h, keep:])
+                assert np.array_equal(de[i, b, h, :len(m)].cpu().numpy(), exps[i, b, h].numpy()[m])
+                assert torch.equal(de[i, b, h, keep:].cpu(), exps[i, b, h, keep:])
+
+
+
+
+def test_evict_reports_a_bad_length():
+    p = bd.kv8_params(1, 1, 64, 16, 64, "f32")
+    codes, exps = random_cache(2, 1, 64, 64, 16, 1)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    acc = torch.rand(2, 1, 4, device=DEV)
+    a0 = acc.clone()
+    n = torch.tensor([65, -1], dtype=torch.int32, device=DEV)
+    kept = torch.empty(2, 1, 2, dtype=torch.int32, device=DEV)
+    bd.csa_kv8_evict(p, 2, 1, acc, n, dc[0], de[0], dc[1], de[1], kept, acc, n)
+    assert bd.device_status() == bd.DEV_BAD_INDEX
+    assert (kept == -1).all() and torch.equal(acc, a0) and n.tolist() == [65, -1]
+    assert torch.equal(dc.cpu(), codes)
+
+
+# ------------------------------------------------------------ run together --
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_a_decode_run_with_eviction(act):
+    """A prompt and a decode period: norm and rotation, append, attention with
+    accumulated weights, eviction whenever a block over budget opens; every
+    stage against the oracle on the stage's own inputs, the cache, lengths
+    and weights carried along on the GPU alone."""
+    B, n_q, n_kv, d, block, N, keep, recent, prompt, steps = 2, 4, 2, 64, 16, 96, 4, 2, 60, 40
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    rope = bd.rope_params(d, 32, layout="half")
+    turns = bd.csa_rope_freqs(rope)
+    g = torch.Generator().manual_seed(21)
+    kc, vc = (torch.zeros(B, n_kv, N, d, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ke, ve = (torch.zeros(B, n_kv, N // block, dtype=torch.uint8, device=DEV) for _ in range(2))
+    acc = torch.zeros(B, n_kv, N // block, device=DEV)
+    n_tok = torch.zeros(B, dtype=torch.int32, device=DEV)
+    kept = torch.empty(B, n_kv, keep, dtype=torch.int32, device=DEV)
+    c = [kc.cpu().numpy(), ke.cpu().numpy(), vc.cpu().numpy(), ve.cpu().numpy()]
+    w, n, at = np.zeros(acc.shape), np.zeros(B, int), 0
+    for step in range(steps):
+        T = prompt if step == 0 else 1
+        qkv = torch.randn(B * T, (n_q + 2 * n_kv) * d, generator=g).to(DT[act]).to(DEV)
+        q, k = qkv[:, :n_q * d].view(-1, n_q, d), qkv[:, n_q * d:(n_q + n_kv) * d].view(-1, n_kv, d)
+        v = qkv[:, (n_q + n_kv) * d:].view(B, T, n_kv, d)
+        qo, ko = torch.empty(B * T, n_q, d, dtype=DT[act], device=DEV), torch.empty(B * T, n_kv, d, dtype=DT[act], device=DEV)
+        pos = torch.arange(at, at + T, dtype=torch.int32, device=DEV).repeat(B)
+        bd.csa_qk_norm_rope(rope, turns, pos, q, k, qo, ko)
+        bd.csa_kv8_append(p, ko.view(B, T, n_kv, d), v, n_tok, kc, ke, vc, ve)
+        vis = (n_tok[:, None] + 1 + torch.arange(T, dtype=torch.int32, device=DEV)).to(torch.int32).view(-1)
+        n_tok += T
+        out = torch.empty_like(qo)
+        bd.csa_kv8_attend(p, qo, vis, kc, ke, vc, ve, out, acc=acc, decay=0.9)
+        kv8.append(np64(ko).reshape(B, T, n_kv, d), n, [T] * B, c[0], c[1], block)
+        kv8.append(np64(v), n, [T] * B, c[2], c[3], block)
+        K, V = kv8.values(c[0], c[1], block), kv8.values(c[2], c[3], block)
+        ref, wr, mag, load = kv8.attend(np64(qo), vis.tolist(), K, V, block, d ** -0.5)
+        within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()) + 1e-30, f"step {step}")
+        n, at = n + T, at + T
+        seen = np.arange(N // block) * block < n[:, None, None]
+        w = np.where(seen, 0.9 * w, w) + wr
+        # 40 steps of relative error 2 eps + sums, each fading by 0.9: below 10 of one step
+        eps = 2 * (2 * d + 24) * U * load.max() + (N + T * n_q) * U
+        within(np64(acc), w, 10 * eps * w + 1e-30, f"acc at step {step}")
+        if n[0] > keep * block:
+            bd.csa_kv8_evict(p, keep, recent, acc, n_tok, kc, ke, vc, ve, kept, acc, n_tok)
+            kr, _, n = kv8.evict(w, n, keep, recent, block)
+            assert np.array_equal(kept.cpu().numpy(), kr), f"step {step}"
+            for b in range(B):
+                for h in range(n_kv):
+                    w[b, h, :keep], w[b, h, keep:] = w[b, h, kr[b, h]], 0.0
+                    for codes, exps in ((c[0], c[1]), (c[2], c[3])):
+                        blocks = codes[b, h].reshape(N // block, block, d)
+                        blocks[:keep] = blocks[kr[b, h]]
+                        exps[b, h, :keep] = exps[b, h][kr[b, h]]
+            assert n_tok.tolist() == n.tolist()
+    live = n[0]
+    assert np.array_equal(kc.cpu().numpy()[:, :, :live], c[0][:, :, :live])
