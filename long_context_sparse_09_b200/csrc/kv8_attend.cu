@@ -1,115 +1,660 @@
 // kv8_attend.cu -- grouped-query attention over the 8-bit KV cache
-// (csa_kv8_attend).
+// (csa_kv8_attend), the form for few query rows a KV head (decode).
 //
-// Simple form: a CTA owns one query row and head.  It walks the visible slots
-// in tiles of one per thread with a running maximum and sum (base 2), a
-// thread scoring a slot and then summing p * value for its dims.  For the
-// accumulated weights it notes the log2 of every block's weight sum and of
-// the row's denominator; kv8_acc adds them up in a fixed order.
+// With x = scale log2(e) q . k (codes of the key times 2^ke) and y = x + ve
+// (ve: the exponent of the value's block) the output is
+//   sum_n 2^(y_n - M) c_n / sum_n 2^(y_n - ve_n - M),   M >= max y - 4,
+// c_n the value's codes: E4M3 codes are exact in fp16, so both products run
+// on codes as they are and every power of two goes into an exponent.  q is
+// held as fp16 times a power of two per row (bf16 queries exactly; fp32 ones
+// as two fp16 terms), p = 2^(y - M + 11) as one or two fp16 terms: the factor
+// 2^11 uses fp16's range up to 2^15, so p keeps 11 bits down to 2^-25 of the
+// row's largest term.
+//
+// What bounds it: the bytes of the cache, read once.  A CTA of 8 warps works
+// on one KV head and 16 query rows (heads of the group x queries); a unit is
+// one tile of 32 slots per warp.  All units of the call lie on one line, cut
+// into equal ranges, one per SM, so ragged lengths and any number of heads
+// fill the machine evenly; the pieces of a head that ends up in several CTAs
+// are joined by kv8_combine.  Each warp feeds itself: its lane 0 loads the
+// tiles with TMA (128-byte swizzle: conflict-free fragment reads) into a ring
+// of its own, and no barrier of the CTA is in the loop.  Both products are
+// mma.sync m16n8k16: at 16 rows a head the loop needs about a third of that
+// path's rate to keep up with HBM, and its operands come from registers, where
+// the codes are widened, without a way through shared or tensor memory.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kv8.h"
+#include "sm100.cuh"
 
 namespace csa {
 
+using namespace sm100;
+
+bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                    uint32_t box_rows);
+bool tma_available();
+
 namespace {
 
-constexpr int kSimpleThreads = 128;
-constexpr int kAccThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRows = 16;          // query rows of a CTA
+constexpr int kTile = 32;          // slots of a warp's tile
+constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
+constexpr float kPShift = 11.f;
+constexpr int kMaxPlan = 1024;     // (sequence, row tile) pairs that the line of units holds
+constexpr int kAccThreads = 128;
+constexpr int kMaxGrid = 256;      // CTAs whose pieces the workspace holds (148 SMs)
 
 struct Kv8AttnArgs {
   const void* q;
   const int32_t* n_vis;
-  Kv8Cache c;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
   const float* sink;
   void* out;
-  float* blk_log;   // [B][H][Q G][NB] log2 of each block's weight sum (unnormalised)
+  float* blk_log;   // [B][H][Q G][NSB] log2 of each sub-block's weight sum (not normalised)
   float* row_log;   // [B][H][Q G] log2 of the row's denominator
+  float* part_o;    // [grid][2][16][d] pieces of heads that several CTAs share
+  float* part_ml;   // [grid][2][16][2] their M and sum
+  int* plan;        // [E + 1] units before each (sequence, row tile)
   float* acc;
   unsigned* err;
-  int B, Q, H, G, d, N, NB, block;
+  int B, Q, H, G, N, NB, block;
+  int sub, NSB;     // slots of a sub-block: min(block, 32); sub-blocks of N
+  int RT, E, planned;
   float scale2, decay;  // softmax scale times log2(e)
 };
 
-__device__ __forceinline__ float pow2e8(uint8_t e) {
-  return __int_as_float(max((int)e, 1) << 23);
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int clamp_exp(int e) { return min(max(e, -126), 127); }
+
+// four codes (a 32-bit word) -> two fp16 pairs
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSimpleThreads) kv8_attend_simple(Kv8AttnArgs a) {
-  __shared__ float qs[256], ps[kSimpleThreads], red[32];
+template <int D, int SPLIT>
+struct Cfg {
+  static constexpr int NW = D == 256 ? 4 : 8;            // warps
+  static constexpr int threads = NW * 32;
+  static constexpr int unit = NW * kTile;                // slots of a unit
+  static constexpr int kv_bytes = kTile * D;             // one tile of K or V
+  static constexpr int NS = D == 64 ? 4 : 2;             // tiles in a warp's ring
+  static constexpr int steps = D / 16;
+  static constexpr int ring = 0;
+  static constexpr int qfrag = ring + NW * NS * 2 * kv_bytes;
+  static constexpr int merge = qfrag + SPLIT * steps * 32 * 16;
+  static constexpr int ml = merge + NW * kRows * (D + 4) * 4;
+  static constexpr int rows = ml + NW * kRows * 8;       // per row: n_vis, exponent of q
+  static constexpr int plan = rows + kRows * 8;          // units before, n_max: [E + 1], [E]
+  static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
+  static constexpr int total = bars + NW * NS * 8 + 16;
+};
+
+// queries of the rows of row tile rt: rows are query * G + head of the group
+__device__ __forceinline__ int tile_max(const Kv8AttnArgs& a, int b, int rt) {
+  const int j0 = rt * kRows / a.G, j1 = min((rt * kRows + kRows - 1) / a.G, a.Q - 1);
+  int n = 0;
+  for (int j = j0; j <= j1; ++j) {
+    const int v = a.n_vis[(int64_t)b * a.Q + j];
+    if (v > a.N) atomicOr(a.err, CSA_DEV_BAD_INDEX);
+    n = max(n, min(v, a.N));
+  }
+  return n;
+}
+
+// CTA c of `grid` takes the units [cut(c), cut(c + 1)) of the line; grid is at
+// most total, so every range holds a unit (the launch may have more CTAs)
+__device__ __forceinline__ long long cut(long long c, long long total, int grid) {
+  return c * total / grid;
+}
+
+// A walk along the line of units; a unit is one tile for every warp.
+struct Cursor {
+  int e, h, local, units, n;  // (sequence, row tile), KV head, unit in it, its units, n_max
+  __device__ __forceinline__ void load(const int* before, const int* nmax) {
+    units = before[e + 1] - before[e];
+    n = nmax[e];
+  }
+  __device__ __forceinline__ void next(const int* before, const int* nmax, int H, int E) {
+    if (++local < units) return;
+    local = 0;
+    if (++h < H) return;
+    h = 0;
+    do { ++e; } while (e < E && before[e + 1] == before[e]);
+    if (e < E) load(before, nmax);
+  }
+};
+
+template <typename T, int D, int SPLIT>
+__global__ void __launch_bounds__(Cfg<D, SPLIT>::threads, 1)
+kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               Kv8AttnArgs a) {
+  using C = Cfg<D, SPLIT>;
+  constexpr int NT = D / 8;  // output n-tiles
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ring = sm + C::ring;
+  uint4* qfrag = reinterpret_cast<uint4*>(sm + C::qfrag);
+  float* mrg = reinterpret_cast<float*>(sm + C::merge);
+  float2* ml = reinterpret_cast<float2*>(sm + C::ml);
+  int2* rowinfo = reinterpret_cast<int2*>(sm + C::rows);
+  int* before = reinterpret_cast<int*>(sm + C::plan);
+  int* nmax = before + kMaxPlan + 1;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::bars);
+  volatile int* abort_sm = reinterpret_cast<volatile int*>(bars + C::NW * C::NS);
+  __shared__ unsigned scan_sh[33];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  if (tid == 0) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    *abort_sm = 0;
+    for (int i = 0; i < C::NW * C::NS; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
   pdl_wait();
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / (a.H * a.G);  // b Q + j
-  const int hq = (int)(blockIdx.x % (a.H * a.G)), h = hq / a.G, b = (int)(row / a.Q);
-  int n = a.n_vis[row];
-  if (n > a.N && tid == 0) atomicOr(a.err, CSA_DEV_BAD_INDEX);
-  n = min(max(n, 0), a.N);
-  const T* q = reinterpret_cast<const T*>(a.q) + (row * a.H * a.G + hq) * a.d;
-  for (int i = tid; i < a.d; i += kSimpleThreads) qs[i] = to_f32(q[i]) * a.scale2;
-  __syncthreads();
-  const int64_t head = (int64_t)b * a.H + h;
-  const int64_t lrow = head * a.Q * a.G + (int64_t)(row % a.Q) * a.G + hq % a.G;
-  const uint8_t* kc = a.c.kc + head * a.N * a.d;
-  const uint8_t* vc = a.c.vc + head * a.N * a.d;
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int s0 = 0; s0 < n; s0 += kSimpleThreads) {
-    const int s = s0 + tid;
-    float x = -INFINITY;
-    if (s < n) {
-      x = 0.f;
-      for (int i = 0; i < a.d; ++i) x = fmaf(qs[i], e4m3_to_f32(kc[(int64_t)s * a.d + i]), x);
-      x *= pow2e8(a.c.k_exp[head * a.NB + s / a.block]);
+  pdl_trigger();
+  // ---- the line of units (or this CTA's one item)
+  long long u0, u1;
+  int e_base = 0;  // (sequence, row tile) of the line's first entry
+  Cursor cur;
+  if (a.planned) {
+    const int per = (a.E + C::threads - 1) / C::threads;
+    const int e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
+    unsigned mine = 0, all;
+    for (int e = e0; e < e1; ++e) {
+      const int n = tile_max(a, e / a.RT, e % a.RT);
+      nmax[e] = n;
+      mine += (unsigned)((n + C::unit - 1) / C::unit);
     }
-    const float m1 = fmaxf(m, block_reduce<true>(x, red));
-    const float p = s < n ? exp2f(x - m1) : 0.f, f = exp2f(m - m1);
-    ps[tid] = p;
-    l = l * f + block_reduce<false>(p, red);
-    if (a.blk_log && tid * a.block < kSimpleThreads && s0 + tid * a.block < n) {
-      float t = 0.f;
-      for (int i = 0; i < a.block; ++i) t += ps[tid * a.block + i];
-      a.blk_log[lrow * a.NB + s0 / a.block + tid] = log2f(t) + m1;
+    unsigned at = block_exclusive_scan(mine, scan_sh, &all);
+    for (int e = e0; e < e1; ++e) {
+      before[e] = (int)at;
+      at += (unsigned)((nmax[e] + C::unit - 1) / C::unit);
     }
-    for (int k = 0; k < 2; ++k) {
-      const int i = tid + k * kSimpleThreads;
-      o[k] *= f;
-      if (i < a.d)
-        for (int t = 0; t < min(kSimpleThreads, n - s0); ++t)
-          o[k] = fmaf(ps[t] * pow2e8(a.c.v_exp[head * a.NB + (s0 + t) / a.block]),
-                      e4m3_to_f32(vc[(int64_t)(s0 + t) * a.d + i]), o[k]);
-    }
-    m = m1;
+    if (tid == 0) before[a.E] = (int)all;
     __syncthreads();
+    if (blockIdx.x == 0)
+      for (int e = tid; e <= a.E; e += C::threads) a.plan[e] = before[e];
+    const long long total = (long long)all * a.H;
+    const int grid = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x >= grid) return;
+    u0 = cut(blockIdx.x, total, grid);
+    u1 = cut(blockIdx.x + 1, total, grid);
+    int lo = 0, hi = a.E;  // the last e with H * before[e] <= u0 that has units
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)before[mid] * a.H <= u0) lo = mid; else hi = mid;
+    }
+    cur.e = lo;
+    cur.load(before, nmax);
+    const int off = (int)(u0 - (long long)before[lo] * a.H);
+    cur.h = off / cur.units;
+    cur.local = off % cur.units;
+  } else {
+    // one item a CTA, all of its units
+    const int e = (int)(blockIdx.x / a.H);
+    if (tid == 0) {
+      const int n = tile_max(a, e / a.RT, e % a.RT);
+      before[0] = 0;
+      before[1] = (n + C::unit - 1) / C::unit;
+      nmax[0] = n;
+    }
+    __syncthreads();
+    e_base = e;
+    cur.e = 0;
+    cur.h = (int)(blockIdx.x % a.H);
+    cur.local = 0;
+    cur.load(before, nmax);
+    u0 = 0;
+    u1 = max(cur.units, 1);  // an item without slots still writes its zeros
   }
-  if (a.sink && n > 0) {
-    const float z = a.sink[hq] * kLog2e, m1 = fmaxf(m, z), f = exp2f(m - m1);
-    l = l * f + exp2f(z - m1);
-    o[0] *= f;
-    o[1] *= f;
-    m = m1;
+  // ---- this warp's loads
+  Cursor pre = cur;
+  long long up = u0;
+  int issued = 0, used = 0;
+  uint8_t* my_ring = ring + warp * C::NS * 2 * C::kv_bytes;
+  uint64_t* my_bars = bars + warp * C::NS;
+  const uint64_t policy = l2_evict_first_policy();
+  auto advance = [&]() {  // issue the loads of the next unit's tile
+    if (up >= u1) return;
+    const int s0 = (pre.local * C::NW + warp) * kTile;
+    if (s0 < pre.n) {
+      if (lane == 0) {
+        const int st = issued % C::NS;
+        uint8_t* dst = my_ring + st * 2 * C::kv_bytes;
+        const int64_t row = ((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + s0;
+        mbar_expect_tx(&my_bars[st], 2 * C::kv_bytes);
+        if constexpr (D == 64) {  // two slots a 128-byte row
+          tma_load_2d_hint(dst, &tmK, &my_bars[st], 0, (int)(row >> 1), policy);
+          tma_load_2d_hint(dst + C::kv_bytes, &tmV, &my_bars[st], 0, (int)(row >> 1), policy);
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < D / 128; ++hf) {
+            tma_load_2d_hint(dst + hf * kTile * 128, &tmK, &my_bars[st], hf * 64, (int)row, policy);
+            tma_load_2d_hint(dst + C::kv_bytes + hf * kTile * 128, &tmV, &my_bars[st], hf * 64,
+                             (int)row, policy);
+          }
+        }
+      }
+      ++issued;
+    }
+    if (++up < u1) pre.next(before, nmax, a.H, a.E);
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::NS; ++i) advance();
+
+  long long u = u0;
+  int segment = 0;
+  while (u < u1) {
+    // ---- a segment: the units of this range that belong to one item
+    const int h = cur.h, b = (cur.e + e_base) / a.RT, rt = (cur.e + e_base) % a.RT;
+    const int local0 = cur.local, units = cur.units;
+    const int count = (int)min((long long)(units - local0), u1 - u);
+    const int64_t head = (int64_t)b * a.H + h;
+    __syncthreads();  // the previous segment's queries and merge area are free
+    for (int r = warp; r < kRows; r += C::NW) {
+      const int rho = rt * kRows + r, j = rho / a.G, hq = h * a.G + rho % a.G;
+      const bool live = rho < a.Q * a.G;
+      const int64_t qrow = (int64_t)b * a.Q + j;
+      const T* q = reinterpret_cast<const T*>(a.q) + (qrow * a.H * a.G + hq) * D;
+      float v[D / 32];
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        v[i] = live ? to_f32(q[i * 32 + lane]) : 0.f;
+        const float f = fabsf(v[i]);
+        amax = fmaxf(amax, f < INFINITY ? f : 0.f);
+      }
+      amax = warp_max(amax);
+      // q * 2^-qe has its largest magnitude in [2^14, 2^15)
+      const int qe = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 - 14 : 0;
+      const float f1 = pow2i(clamp_exp(-qe)), f2 = pow2i(-qe - clamp_exp(-qe));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int x = i * 32 + lane, xx = x % 128, c = xx / 16, y = xx % 16, z = y & 3;
+        const int tt = D == 64 ? c : c >> 1;
+        const int s = (D == 64 ? 0 : (x / 128) * 8 + (c & 1) * 4) + (y >> 2);
+        const int idx = ((s * 32 + (r & 7) * 4 + tt) * 4 + (z >> 1) * 2 + (r >> 3)) * 2 + (z & 1);
+        const float f = v[i] * f1 * f2;
+        const __half hi = __float2half_rn(f);
+        reinterpret_cast<__half*>(qfrag)[idx] = hi;
+        if constexpr (SPLIT == 2)
+          reinterpret_cast<__half*>(qfrag + C::steps * 32)[idx] = __float2half_rn(f - __half2float(hi));
+      }
+      if (lane == 0) rowinfo[r] = make_int2(live ? min(a.n_vis[qrow], a.N) : 0, qe);
+    }
+    __syncthreads();
+    const int2 inf0 = rowinfo[g], inf1 = rowinfo[g + 8];
+    const int vis[2] = {inf0.x, inf1.x}, qe[2] = {inf0.y, inf1.y};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    const uint8_t* ke_p = a.k_exp + head * a.NB;
+    const uint8_t* ve_p = a.v_exp + head * a.NB;
+
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int s0 = ((local0 + i) * C::NW + warp) * kTile;
+      if (s0 >= cur.n) {  // beyond the item's last slot
+        advance();
+        continue;
+      }
+      // exponents of the tile's two halves (a tile may end beyond the cache)
+      const int i0 = s0 / a.block, i1 = min((s0 + 16) / a.block, a.NB - 1);
+      const int ke[2] = {(int)ke_p[i0] - 127, (int)ke_p[i1] - 127};
+      const int ve[2] = {(int)ve_p[i0] - 127, (int)ve_p[i1] - 127};
+      const int st = used % C::NS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&my_bars[st], (used / C::NS) & 1, abort_sm))) break;
+      ++used;
+      const uint8_t* ks = my_ring + st * 2 * C::kv_bytes;
+      const uint8_t* vs = ks + C::kv_bytes;
+      // ---- S = q K^T over codes
+      float s[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
+#pragma unroll
+      for (int hc = 0; hc < (D == 64 ? 1 : D / 64); ++hc) {  // 16-byte chunks of a slot's row
+        uint4 kw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tok = 8 * j + g;
+          const uint8_t* p;
+          if constexpr (D == 64)
+            p = ks + (tok >> 1) * 128 + ((((tok & 1) * 4 + t) ^ ((tok >> 1) & 7)) << 4);
+          else
+            p = ks + (hc >> 1) * kTile * 128 + tok * 128 + (((2 * t + (hc & 1)) ^ (tok & 7)) << 4);
+          kw[j] = *reinterpret_cast<const uint4*>(p);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint4 qa = qfrag[(hc * 4 + w) * 32 + lane];
+          uint4 qb;
+          if constexpr (SPLIT == 2) qb = qfrag[(C::steps + hc * 4 + w) * 32 + lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t b0, b1;
+            widen4(w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w, b0, b1);
+            mma_f16(s[j], qa, b0, b1);
+            if constexpr (SPLIT == 2) mma_f16(s[j], qb, b0, b1);
+          }
+        }
+      }
+      // ---- y = x + ve, running maximum
+      float tmax[2] = {-INFINITY, -INFINITY};
+      const bool whole = __all_sync(0xffffffffu, min(vis[0], vis[1]) >= s0 + kTile);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float c = a.scale2 * pow2i(clamp_exp(qe[r] + ke[j >> 1]));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float y = fmaf(s[j][2 * r + k], c, (float)ve[j >> 1]);
+            if (!whole && s0 + 8 * j + 2 * t + k >= vis[r]) y = -INFINITY;
+            s[j][2 * r + k] = y;
+            tmax[r] = fmaxf(tmax[r], y);
+          }
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], 1));
+        tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], 2));
+      }
+      if (__any_sync(0xffffffffu, tmax[0] > m[0] + kLazy || tmax[1] > m[1] + kLazy)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float m1 = fmaxf(m[r], tmax[r]);
+          const float f = m1 > m[r] ? fast_exp2(m[r] - m1) : 1.f;
+          m[r] = m1;
+          l[r] *= f;
+#pragma unroll
+          for (int i2 = 0; i2 < NT; ++i2) {
+            o[i2][2 * r] *= f;
+            o[i2][2 * r + 1] *= f;
+          }
+        }
+      }
+      // ---- p = 2^(y - m + 11), its sums by half tile
+      float half_sum[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float sub = m[r] == -INFINITY ? 0.f : m[r] - kPShift;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 2 * hh; j < 2 * hh + 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              s[j][2 * r + k] = fast_exp2(s[j][2 * r + k] - sub);
+              sum += s[j][2 * r + k];
+            }
+          half_sum[r][hh] = sum;
+          l[r] = fmaf(sum * 0x1p-11f, pow2i(clamp_exp(-ve[hh])), l[r]);
+        }
+      }
+      if (a.blk_log) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float h0 = half_sum[r][0], h1 = half_sum[r][1];
+          h0 += __shfl_xor_sync(0xffffffffu, h0, 1);
+          h1 += __shfl_xor_sync(0xffffffffu, h1, 1);
+          h0 += __shfl_xor_sync(0xffffffffu, h0, 2);
+          h1 += __shfl_xor_sync(0xffffffffu, h1, 2);
+          const int rho = rt * kRows + g + 8 * r;
+          if (t == 0 && vis[r] > s0) {
+            float* dst = a.blk_log + (head * a.Q * a.G + rho) * a.NSB + s0 / a.sub;
+            const float base = m[r] - kPShift;
+            if (a.sub == 32) {
+              dst[0] = log2f(h0 + h1) + (base - ve[0]);
+            } else {
+              dst[0] = log2f(h0) + (base - ve[0]);
+              if (vis[r] > s0 + 16) dst[1] = log2f(h1) + (base - ve[1]);
+            }
+          }
+        }
+      }
+      // ---- O += p V over codes; slots no row sees hold anything: zeros
+      const int lim = cur.n - s0;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint4 pa, pb;
+        pa.x = pack_h2(s[2 * hh][0], s[2 * hh][1]);
+        pa.y = pack_h2(s[2 * hh][2], s[2 * hh][3]);
+        pa.z = pack_h2(s[2 * hh + 1][0], s[2 * hh + 1][1]);
+        pa.w = pack_h2(s[2 * hh + 1][2], s[2 * hh + 1][3]);
+        if constexpr (SPLIT == 2) {
+          auto rest = [](uint32_t hi, float x, float y) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            return pack_h2(x - f.x, y - f.y);
+          };
+          pb.x = rest(pa.x, s[2 * hh][0], s[2 * hh][1]);
+          pb.y = rest(pa.y, s[2 * hh][2], s[2 * hh][3]);
+          pb.z = rest(pa.z, s[2 * hh + 1][0], s[2 * hh + 1][1]);
+          pb.w = rest(pa.w, s[2 * hh + 1][2], s[2 * hh + 1][3]);
+        }
+        constexpr int VW = D == 64 ? 2 : 4;  // words of a slot's chunk
+#pragma unroll
+        for (int hf = 0; hf < (D == 256 ? 2 : 1); ++hf) {
+          uint32_t vw[4][VW];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = 16 * hh + 2 * t + (k & 1) + (k >> 1) * 8;
+            if constexpr (D == 64) {
+              const int row = tok >> 1, ch = (tok & 1) * 4 + (g >> 1);
+              const uint2 v2 = *reinterpret_cast<const uint2*>(vs + row * 128 + ((ch ^ (row & 7)) << 4) + (g & 1) * 8);
+              vw[k][0] = v2.x;
+              vw[k][1] = v2.y;
+            } else {
+              const uint4 v4 = *reinterpret_cast<const uint4*>(vs + hf * kTile * 128 + tok * 128 + ((g ^ (tok & 7)) << 4));
+              vw[k][0] = v4.x;
+              vw[k][1] = v4.y;
+              vw[k][VW - 2] = v4.z;
+              vw[k][VW - 1] = v4.w;
+            }
+            if (lim < kTile && tok >= lim)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vw[k][w] = 0;
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            // pair the slots' bytes dim by dim: (slot 2t, slot 2t + 1) of dims 4w .. 4w + 3
+            uint32_t b0[4], b1[4];
+            widen4(__byte_perm(vw[0][w], vw[1][w], 0x5140), b0[0], b0[1]);
+            widen4(__byte_perm(vw[0][w], vw[1][w], 0x7362), b0[2], b0[3]);
+            widen4(__byte_perm(vw[2][w], vw[3][w], 0x5140), b1[0], b1[1]);
+            widen4(__byte_perm(vw[2][w], vw[3][w], 0x7362), b1[2], b1[3]);
+#pragma unroll
+            for (int d4 = 0; d4 < 4; ++d4) {
+              float(&acc)[4] = o[hf * 16 + w * 4 + d4];
+              mma_f16(acc, pa, b0[d4], b1[d4]);
+              if constexpr (SPLIT == 2) mma_f16(acc, pb, b0[d4], b1[d4]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the tile is read
+      advance();
+    }
+
+    // ---- the warps' pieces become one
+    u += max(count, 1);
+    const bool complete = count == units;
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      float* dst = mrg + (warp * kRows + g + 8 * r) * (D + 4);
+      if (t == 0) ml[warp * kRows + g + 8 * r] = make_float2(m[r], l[r]);
+      // n-tile (hf, w): column 2t is dim 128 hf + (D == 64 ? 8 : 16) 2t + w
+      constexpr int CH = D == 64 ? 8 : 16;
+#pragma unroll
+      for (int hf = 0; hf < (D == 256 ? 2 : 1); ++hf)
+#pragma unroll
+        for (int w = 0; w < CH; w += 4)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(dst + hf * 128 + CH * (2 * t + k) + w) =
+                make_float4(o[hf * CH + w][2 * r + k], o[hf * CH + w + 1][2 * r + k],
+                            o[hf * CH + w + 2][2 * r + k], o[hf * CH + w + 3][2 * r + k]);
+    }
+    __syncthreads();
+    {
+      constexpr int TPR = C::threads / kRows;  // threads of a row
+      const int r = tid / TPR, rho = rt * kRows + r;
+      float M = -INFINITY, L = 0.f, f[C::NW];
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) {
+        const float2 v = ml[w * kRows + r];
+        f[w] = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
+        L = fmaf(v.y, f[w], L);
+      }
+      const bool live = rho < a.Q * a.G;
+      float inv = 0.f;
+      const int j = rho / a.G, hq = h * a.G + rho % a.G;
+      if (complete && live) {
+        if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - M);
+        inv = rowinfo[r].x > 0 ? 0x1p-11f / L : 0.f;
+        if (a.row_log && tid % TPR == 0) a.row_log[head * a.Q * a.G + rho] = log2f(L) + M;
+      }
+      const int64_t slot = (int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1);
+      if (!complete && tid % TPR == 0) reinterpret_cast<float2*>(a.part_ml)[slot * kRows + r] = make_float2(M, L);
+      T* out = reinterpret_cast<T*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * D;
+      float* part = a.part_o + (slot * kRows + r) * D;
+#pragma unroll 1
+      for (int c = (tid % TPR) * 4; c < D; c += TPR * 4) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(mrg + (w * kRows + r) * (D + 4) + c);
+          sum.x = fmaf(v.x, f[w], sum.x);
+          sum.y = fmaf(v.y, f[w], sum.y);
+          sum.z = fmaf(v.z, f[w], sum.z);
+          sum.w = fmaf(v.w, f[w], sum.w);
+        }
+        if (!complete) {
+          *reinterpret_cast<float4*>(part + c) = sum;
+        } else if (live) {
+          if (rowinfo[r].x <= 0) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          else sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(out + c) = sum;
+          } else {
+            __nv_bfloat162 h2[2] = {__floats2bfloat162_rn(sum.x, sum.y), __floats2bfloat162_rn(sum.z, sum.w)};
+            *reinterpret_cast<uint2*>(out + c) = *reinterpret_cast<uint2*>(h2);
+          }
+        }
+      }
+    }
+    ++segment;
+    cur.local = local0 + count - 1;
+    if (u < u1) cur.next(before, nmax, a.H, a.E);
+    if (*abort_sm) break;
   }
-  if (a.row_log && tid == 0) a.row_log[lrow] = n > 0 ? log2f(l) + m : 0.f;
-  T* out = reinterpret_cast<T*>(a.out) + (row * a.H * a.G + hq) * a.d;
-  for (int k = 0; k < 2; ++k) {
-    const int i = tid + k * kSimpleThreads;
-    if (i < a.d) out[i] = from_f32<T>(n > 0 ? o[k] / l : 0.f);
+  if (*abort_sm && lane == 0) {
+    atomicOr(a.err, CSA_DEV_TIMEOUT);
+    const uint64_t t0 = globaltimer();  // loads already issued land before the CTA leaves
+    while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
   }
 }
 
+// Joins the pieces of the heads that several CTAs share; one CTA a row.  Rows
+// of sequences without slots get their zeros here.
+template <typename T>
+__global__ void kv8_combine(Kv8AttnArgs a, int d, int grid) {
+  pdl_wait();
+  const int r = (int)(blockIdx.x % kRows);
+  const int64_t item = blockIdx.x / kRows;
+  const int e = (int)(item / a.H), h = (int)(item % a.H), b = e / a.RT, rt = e % a.RT;
+  const int rho = rt * kRows + r;
+  if (rho >= a.Q * a.G) return;
+  const int j = rho / a.G, hq = h * a.G + rho % a.G;
+  T* out = reinterpret_cast<T*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * d;
+  const int units = a.plan[e + 1] - a.plan[e];
+  if (units == 0) {
+    for (int c = threadIdx.x; c < d; c += blockDim.x) out[c] = from_f32<T>(0.f);
+    return;
+  }
+  const long long total = (long long)a.plan[a.E] * a.H;
+  grid = (int)min((long long)grid, total);
+  const long long U0 = (long long)a.plan[e] * a.H + (long long)h * units, U1 = U0 + units;
+  // the CTAs whose ranges hold the item's first and last unit
+  const int c0 = (int)(((U0 + 1) * grid - 1) / total), c1 = (int)((U1 * grid - 1) / total);
+  if (c0 == c1) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  auto slot = [&](int c) {  // a CTA's first segment is piece 0, its last piece 1
+    return (int64_t)c * 2 + (cut(c, total, grid) >= U0 ? 0 : 1);
+  };
+  float M = -INFINITY;
+  for (int c = c0 + (int)threadIdx.x; c <= c1; c += blockDim.x) M = fmaxf(M, ml[slot(c) * kRows + r].x);
+  __shared__ float red[32];
+  M = block_reduce<true>(M, red);
+  float L = 0.f, sum = 0.f;
+  const bool mine = (int)threadIdx.x < d;
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t sl = slot(c);
+    const float2 v = ml[sl * kRows + r];
+    const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
+    L = fmaf(v.y, f, L);
+    if (mine) sum = fmaf(a.part_o[(sl * kRows + r) * d + threadIdx.x], f, sum);
+  }
+  if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - M);
+  const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
+  if (a.row_log && threadIdx.x == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + M;
+  if (mine) out[threadIdx.x] = from_f32<T>(sees ? sum * (0x1p-11f / L) : 0.f);
+}
+
+// acc = decay acc + sum over the KV head's rows of the weight on a block
 __global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(Kv8AttnArgs a, int tiles) {
   pdl_wait();
   const int64_t head = blockIdx.x / tiles;
   const int i = (int)(blockIdx.x % tiles) * kAccThreads + threadIdx.x;
   if (i >= a.NB) return;
-  const int b = (int)(head / a.H);
+  const int b = (int)(head / a.H), per = a.block / a.sub;
   float sum = 0.f;
   bool seen = false;
   for (int j = 0; j < a.Q; ++j) {
-    if ((int64_t)i * a.block >= min(a.n_vis[(int64_t)b * a.Q + j], a.N)) continue;
+    const int n = min(a.n_vis[(int64_t)b * a.Q + j], a.N);
+    const int left = n - i * a.block;  // slots of the block that the query sees
+    if (left <= 0) continue;
     seen = true;
+    const int subs = min(per, (left + a.sub - 1) / a.sub);
     for (int g = 0; g < a.G; ++g) {
       const int64_t lrow = (head * a.Q + j) * a.G + g;
-      sum += exp2f(a.blk_log[lrow * a.NB + i] - a.row_log[lrow]);
+      const float den = a.row_log[lrow];
+      for (int k = 0; k < subs; ++k)
+        sum += fast_exp2(a.blk_log[lrow * a.NSB + (int64_t)i * per + k] - den);
     }
   }
   if (!seen) return;
@@ -117,43 +662,107 @@ __global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(Kv8AttnArgs a, int
   *acc = a.decay == 0.f ? sum : fmaf(a.decay, *acc, sum);
 }
 
+struct Ws {
+  size_t plan, part_ml, part_o, row_log, blk_log, total;
+};
+
+Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
+  const size_t rows = (size_t)B * Q * p.n_q;
+  const int grid = kMaxGrid;
+  Ws w;
+  w.plan = 0;
+  w.part_ml = w.plan + align_up((kMaxPlan + 1) * 4, 256);
+  w.part_o = w.part_ml + (size_t)grid * 2 * kRows * 8;
+  w.row_log = w.part_o + (size_t)grid * 2 * kRows * p.d * 4;
+  w.blk_log = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
+  w.total = w.blk_log + (acc ? align_up(rows * (p.N / (p.block < 32 ? p.block : 32)) * 4, 256) : 0);
+  return w;
+}
+
+template <typename T, int D, int SPLIT>
+csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, Kv8AttnArgs& a, cudaStream_t st) {
+  using C = Cfg<D, SPLIT>;
+  CUtensorMap tmK, tmV;
+  const uint64_t slots = (uint64_t)a.B * a.H * a.N;
+  const uint64_t rows = D == 64 ? slots / 2 : slots, cols = D == 64 ? 64 : D / 2;
+  const uint32_t box = D == 64 ? kTile / 2 : kTile;
+  if (!make_tmap_bf16(&tmK, c.kc, rows, cols, box) || !make_tmap_bf16(&tmV, c.vc, rows, cols, box))
+    return CSA_ERR_CUDA;
+  auto kern = kv8_attend_mma<T, D, SPLIT>;
+  const int smem = C::total + 1024;
+  if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
+  // one line of units over all SMs; so many row tiles that they fill the
+  // machine anyway: a CTA each
+  const long long items = (long long)a.E * a.H;
+  a.planned = a.E <= kMaxPlan;
+  long long grid = items;
+  if (a.planned) {
+    const long long units = items * ((a.N + C::unit - 1) / C::unit);
+    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    if (units < grid) grid = units;
+  }
+  if (grid > 0x7fffffffll || items * kRows > 0x7fffffffll) return CSA_ERR_SHAPE;
+  csa_status ok = CSA_OK;
+  CSA_LAUNCH(KK_KV8_ATTEND, st,
+             if (launch_maybe_pdl(true, kern, dim3((unsigned)grid), dim3(C::threads), smem, st, tmK,
+                                  tmV, a) != cudaSuccess) ok = CSA_ERR_CUDA);
+  if (a.planned)
+    CSA_LAUNCH(KK_KV8_COMBINE, st,
+               if (launch_maybe_pdl(true, kv8_combine<T>, dim3((unsigned)(items * kRows)), dim3(D), 0,
+                                    st, a, D, (int)grid) != cudaSuccess) ok = CSA_ERR_CUDA);
+  return ok != CSA_OK ? ok : last_launch_status();
+}
+
 }  // namespace
 
 size_t kv8_attend_ws_bytes(const csa_kv8_params& p, int B, int Q, bool acc) {
-  const size_t rows = (size_t)B * Q * p.n_q;
-  return acc ? align_up(rows * (p.N / p.block) * 4, 256) + align_up(rows * 4, 256) : 0;
+  return layout(p, B, Q, acc).total;
 }
 
 csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale, const void* q,
                              const int32_t* n_vis, const Kv8Cache& c, const float* sink,
                              void* out, float* acc, float decay, void* ws, cudaStream_t st) {
   Kv8AttnArgs a = {};
-  a.q = q; a.n_vis = n_vis; a.c = c; a.sink = sink; a.out = out;
-  a.B = B; a.Q = Q; a.H = p.n_kv; a.G = p.n_q / p.n_kv; a.d = p.d; a.N = p.N;
+  a.q = q; a.n_vis = n_vis; a.k_exp = c.k_exp; a.v_exp = c.v_exp; a.sink = sink; a.out = out;
+  a.B = B; a.Q = Q; a.H = p.n_kv; a.G = p.n_q / p.n_kv; a.N = p.N;
   a.NB = p.N / p.block; a.block = p.block;
+  a.sub = p.block < 32 ? p.block : 32;
+  a.NSB = p.N / a.sub;
+  const long long rts = ((long long)Q * a.G + kRows - 1) / kRows;
+  if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
+  a.RT = (int)rts;
+  a.E = (int)(rts * B);
   a.scale2 = scale * kLog2e;
   a.decay = decay;
   a.err = device_error_word();
   if (a.err == nullptr) return CSA_ERR_CUDA;
-  const size_t rows = (size_t)B * Q * p.n_q;
+  if (!tma_available()) return CSA_ERR_CUDA;
+  const Ws w = layout(p, B, Q, acc != nullptr);
+  char* base = (char*)ws;
+  a.plan = (int*)(base + w.plan);
+  a.part_ml = (float*)(base + w.part_ml);
+  a.part_o = (float*)(base + w.part_o);
   if (acc) {
     a.acc = acc;
-    a.blk_log = (float*)ws;
-    a.row_log = (float*)((char*)ws + align_up(rows * a.NB * 4, 256));
+    a.row_log = (float*)(base + w.row_log);
+    a.blk_log = (float*)(base + w.blk_log);
   }
-  if (rows > 0x7fffffff) return CSA_ERR_SHAPE;
-  auto kern = p.act == CSA_F32 ? kv8_attend_simple<float> : kv8_attend_simple<__nv_bfloat16>;
+  csa_status r;
+  if (p.act == CSA_F32)
+    r = p.d == 64 ? launch_mma<float, 64, 2>(p, c, a, st)
+        : p.d == 128 ? launch_mma<float, 128, 2>(p, c, a, st) : launch_mma<float, 256, 2>(p, c, a, st);
+  else
+    r = p.d == 64 ? launch_mma<__nv_bfloat16, 64, 1>(p, c, a, st)
+        : p.d == 128 ? launch_mma<__nv_bfloat16, 128, 1>(p, c, a, st)
+                     : launch_mma<__nv_bfloat16, 256, 1>(p, c, a, st);
+  if (r != CSA_OK || !acc) return r;
+  const int tiles = (a.NB + kAccThreads - 1) / kAccThreads;
+  if ((long long)B * a.H * tiles > 0x7fffffffll) return CSA_ERR_SHAPE;
   csa_status ok = CSA_OK;
-  CSA_LAUNCH(KK_KV8_ATTEND, st,
-             if (launch_maybe_pdl(true, kern, dim3((unsigned)rows), dim3(kSimpleThreads), 0, st,
-                                  a) != cudaSuccess) ok = CSA_ERR_CUDA);
-  if (acc) {
-    const int tiles = (a.NB + kAccThreads - 1) / kAccThreads;
-    CSA_LAUNCH(KK_KV8_ACC, st,
-               if (launch_maybe_pdl(true, kv8_acc_kernel, dim3((unsigned)(B * a.H * tiles)),
-                                    dim3(kAccThreads), 0, st, a, tiles) != cudaSuccess)
-                 ok = CSA_ERR_CUDA);
-  }
+  CSA_LAUNCH(KK_KV8_ACC, st,
+             if (launch_maybe_pdl(true, kv8_acc_kernel, dim3((unsigned)(B * a.H * tiles)),
+                                  dim3(kAccThreads), 0, st, a, tiles) != cudaSuccess)
+               ok = CSA_ERR_CUDA);
   return ok != CSA_OK ? ok : last_launch_status();
 }
 

@@ -264,8 +264,10 @@ def check_attend(case, seed, decay=1.0):
     dw = None if w is None else w.to(DEV)
     if decay == 0.0 and dw is not None:
         dw.fill_(float("nan"))
+    # nothing in the workspace needs to be set: it starts as NaN
+    ws = torch.full((bd.kv8_attend_workspace_bytes(p, B, Q, acc),), 255, dtype=torch.uint8, device=DEV)
     bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out,
-                      sink=None if z is None else z.to(DEV), acc=dw, decay=decay)
+                      sink=None if z is None else z.to(DEV), acc=dw, decay=decay, workspace=ws)
     exps_ref = np.where(exps.numpy() == 255, 127, exps.numpy())
     K, V = (kv8.values(clean[i].numpy(), exps_ref[i], block) for i in range(2))
     scale = d ** -0.5
