@@ -457,7 +457,7 @@ csa_status csa_qk_norm_rope(const csa_rope* r, int R, int n_q, int n_kv, int act
  *   n_new   [B] int32            tokens of each sequence, <= T (NULL: all T)
  * Tokens beyond slot N are skipped and raise CSA_DEV_BAD_INDEX, as does an
  * n_old outside [0, N] (its sequence is skipped) or an n_new outside [0, T]
- * (clamped). */
+ * (clamped).  B <= 65535. */
 csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, int64_t k_stride,
                           const void* v, int64_t v_stride, const int32_t* n_old,
                           const int32_t* n_new, void* kc, uint8_t* k_exp, void* vc,

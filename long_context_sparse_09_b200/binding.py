@@ -583,16 +583,17 @@ def kv8_params(n_q, n_kv, d, block, N, act) -> CsaKv8Params:
 
 
 def _dense(t, dtype, shape, what, dev):
-    """A contiguous device tensor of that dtype, shape and device; its address."""
+    """A contiguous tensor of that dtype and shape on CUDA device dev (its
+    index); its address."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{what}: on {t.device}, the call is on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous tensor expected")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the call is on cuda:{dev}")
+    raise ValueError(f"{what}: contiguous tensor expected")
 
 
 def _token_stride(t, dtype, what, dev):
@@ -600,8 +601,8 @@ def _token_stride(t, dtype, what, dev):
     of wider ones; a token's heads are contiguous."""
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{what}: on {t.device}, the call is on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the call is on cuda:{dev}")
     R, n, d = t.shape
     sr, sn, sd = t.stride()
     if (sd != 1 and d > 1) or (sn != d and n > 1):
@@ -610,9 +611,10 @@ def _token_stride(t, dtype, what, dev):
 
 
 def _cuda_dev(t, what):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise ValueError(f"{what}: device tensor expected")
-    return t.device
+    return dev
 
 
 def _launch(name, dev, stream, *args):
@@ -620,12 +622,12 @@ def _launch(name, dev, stream, *args):
     stream of that device."""
     fn = getattr(_lib or lib(), name)
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on cuda:{dev}")
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -639,7 +641,7 @@ def csa_rope_freqs(rope: CsaRope, device="cuda", stream=None) -> torch.Tensor:
     turns = torch.empty(rope.rope_dims // 2, dtype=torch.float64, device=device)
     if stream is not None:
         turns.record_stream(stream)
-    _launch("csa_rope_freqs", turns.device, stream, C.byref(rope), turns.data_ptr() or None)
+    _launch("csa_rope_freqs", _cuda_dev(turns, "turns"), stream, C.byref(rope), turns.data_ptr() or None)
     return turns
 
 
@@ -697,13 +699,18 @@ def csa_kv8_append(p: CsaKv8Params, k, v, n_old, kc, k_exp, vc, v_exp, n_new=Non
     T = k.shape[1]
     strides = []
     for t, what in ((k, "k"), (v, "v")):
+        if t.dtype is not act:
+            raise ValueError(f"{what}: {act} expected, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: on {t.device}, the call is on cuda:{dev}")
         if t.shape != (B, T, p.n_kv, p.d):
             raise ValueError(f"{what}: [{B}][{T}][{p.n_kv}][{p.d}] expected, got {tuple(t.shape)}")
-        s = t.stride()
-        if B > 1 and T > 1 and s[0] != T * s[1]:
+        sb, st, sh, sd = t.stride()
+        if sd != 1 or (sh != p.d and p.n_kv > 1):
+            raise ValueError(f"{what}: the heads of a token must be contiguous")
+        if B > 1 and T > 1 and sb != T * st:
             raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
-        strides.append(_token_stride(t[0] if T > 1 else t[:, 0] if T == 1 else t.new_empty(0, p.n_kv, p.d),
-                                     act, what, dev))
+        strides.append(st if T > 1 else sb if B > 1 and T == 1 else p.n_kv * p.d)
     _launch("csa_kv8_append", dev, stream, C.byref(p), B, T, k.data_ptr(), strides[0], v.data_ptr(),
             strides[1], _dense(n_old, torch.int32, (B,), "n_old", dev),
             None if n_new is None else _dense(n_new, torch.int32, (B,), "n_new", dev), *cache)
@@ -730,11 +737,11 @@ def csa_kv8_attend(p: CsaKv8Params, q, n_vis, kc, k_exp, vc, v_exp, out, sink=No
     wp, wb = None, 0
     if need:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             if stream is not None:
                 workspace.record_stream(stream)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: contiguous tensor on {dev} expected")
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous tensor on cuda:{dev} expected")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch("csa_kv8_attend", dev, stream, C.byref(p), B, Q, p.d ** -0.5 if scale is None else scale,
             qp, _dense(n_vis, torch.int32, (R,), "n_vis", dev), *cache,

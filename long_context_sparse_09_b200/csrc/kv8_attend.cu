@@ -64,6 +64,7 @@ struct Kv8AttnArgs {
   unsigned* err;
   int B, Q, H, G, N, NB, block;
   int sub, NSB;     // slots of a sub-block: min(block, 32); sub-blocks of N
+  int shift, sub_shift;  // log2 of block and sub
   int RT, E, planned;
   float scale2, decay;  // softmax scale times log2(e)
 };
@@ -239,30 +240,39 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint8_t* my_ring = ring + warp * C::NS * 2 * C::kv_bytes;
   uint64_t* my_bars = bars + warp * C::NS;
   const uint64_t policy = l2_evict_first_policy();
+  int pre_s0 = 0, pre_row = 0, pre_left = 0;  // next tile's slot, row of the tensor map, units of the item left
+  auto enter = [&]() {
+    pre_s0 = (pre.local * C::NW + warp) * kTile;
+    const int64_t row = ((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + pre_s0;
+    pre_row = (int)(D == 64 ? row >> 1 : row);  // d = 64: two slots a 128-byte row
+    pre_left = pre.units - pre.local;
+  };
+  enter();
   auto advance = [&]() {  // issue the loads of the next unit's tile
     if (up >= u1) return;
-    const int s0 = (pre.local * C::NW + warp) * kTile;
-    if (s0 < pre.n) {
+    if (pre_s0 < pre.n) {
       if (lane == 0) {
         const int st = issued % C::NS;
         uint8_t* dst = my_ring + st * 2 * C::kv_bytes;
-        const int64_t row = ((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + s0;
         mbar_expect_tx(&my_bars[st], 2 * C::kv_bytes);
-        if constexpr (D == 64) {  // two slots a 128-byte row
-          tma_load_2d_hint(dst, &tmK, &my_bars[st], 0, (int)(row >> 1), policy);
-          tma_load_2d_hint(dst + C::kv_bytes, &tmV, &my_bars[st], 0, (int)(row >> 1), policy);
-        } else {
 #pragma unroll
-          for (int hf = 0; hf < D / 128; ++hf) {
-            tma_load_2d_hint(dst + hf * kTile * 128, &tmK, &my_bars[st], hf * 64, (int)row, policy);
-            tma_load_2d_hint(dst + C::kv_bytes + hf * kTile * 128, &tmV, &my_bars[st], hf * 64,
-                             (int)row, policy);
-          }
+        for (int hf = 0; hf < (D == 256 ? 2 : 1); ++hf) {
+          tma_load_2d_hint(dst + hf * kTile * 128, &tmK, &my_bars[st], hf * 64, pre_row, policy);
+          tma_load_2d_hint(dst + C::kv_bytes + hf * kTile * 128, &tmV, &my_bars[st], hf * 64, pre_row,
+                           policy);
         }
       }
       ++issued;
     }
-    if (++up < u1) pre.next(before, nmax, a.H, a.E);
+    if (++up >= u1) return;
+    if (--pre_left > 0) {
+      pre_s0 += C::unit;
+      pre_row += D == 64 ? C::unit / 2 : C::unit;
+    } else {
+      pre.local = pre.units - 1;
+      pre.next(before, nmax, a.H, a.E);
+      enter();
+    }
   };
 #pragma unroll 1
   for (int i = 0; i < C::NS; ++i) advance();
@@ -327,7 +337,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         continue;
       }
       // exponents of the tile's two halves (a tile may end beyond the cache)
-      const int i0 = s0 / a.block, i1 = min((s0 + 16) / a.block, a.NB - 1);
+      const int i0 = s0 >> a.shift, i1 = min((s0 + 16) >> a.shift, a.NB - 1);
       const int ke[2] = {(int)ke_p[i0] - 127, (int)ke_p[i1] - 127};
       const int ve[2] = {(int)ve_p[i0] - 127, (int)ve_p[i1] - 127};
       const int st = used % C::NS;
@@ -377,13 +387,21 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         for (int j = 0; j < 4; ++j) {
           const float c = a.scale2 * pow2i(clamp_exp(qe[r] + ke[j >> 1]));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y = fmaf(s[j][2 * r + k], c, (float)ve[j >> 1]);
-            if (!whole && s0 + 8 * j + 2 * t + k >= vis[r]) y = -INFINITY;
-            s[j][2 * r + k] = y;
-            tmax[r] = fmaxf(tmax[r], y);
-          }
+          for (int k = 0; k < 2; ++k) s[j][2 * r + k] = fmaf(s[j][2 * r + k], c, (float)ve[j >> 1]);
         }
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (s0 + 8 * j + 2 * t + k >= vis[r]) s[j][2 * r + k] = -INFINITY;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmax[r] = fmaxf(tmax[r], fmaxf(s[j][2 * r], s[j][2 * r + 1]));
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], 1));
@@ -432,7 +450,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           h1 += __shfl_xor_sync(0xffffffffu, h1, 2);
           const int rho = rt * kRows + g + 8 * r;
           if (t == 0 && vis[r] > s0) {
-            float* dst = a.blk_log + (head * a.Q * a.G + rho) * a.NSB + s0 / a.sub;
+            float* dst = a.blk_log + (head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
             const float base = m[r] - kPShift;
             if (a.sub == 32) {
               dst[0] = log2f(h0 + h1) + (base - ve[0]);
@@ -443,8 +461,18 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           }
         }
       }
-      // ---- O += p V over codes; slots no row sees hold anything: zeros
+      // ---- O += p V over codes; slots that no row sees may hold anything: the
+      // item's last tile gets zeros there (whole slots, so swizzled rows too)
       const int lim = cur.n - s0;
+      if (lim < kTile) {
+        for (int i = lane; i < C::kv_bytes / 16; i += 32) {
+          const int row = (i * 16 % (kTile * 128)) / 128;
+          const int chunk = (i & 7) ^ (row & 7);  // where it stands before the swizzle
+          const int tok = D == 64 ? 2 * row + (chunk >> 2) : row;
+          if (tok >= lim) reinterpret_cast<uint4*>(my_ring + st * 2 * C::kv_bytes + C::kv_bytes)[i] = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         uint4 pa, pb;
@@ -481,9 +509,6 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
               vw[k][VW - 2] = v4.z;
               vw[k][VW - 1] = v4.w;
             }
-            if (lim < kTile && tok >= lim)
-#pragma unroll
-              for (int w = 0; w < VW; ++w) vw[k][w] = 0;
           }
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
@@ -502,6 +527,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           }
         }
       }
+      if (lim < kTile) fence_proxy_async_smem();  // the zeros before a later load into the tile
       __syncwarp();  // the tile is read
       advance();
     }
@@ -728,6 +754,8 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   a.NB = p.N / p.block; a.block = p.block;
   a.sub = p.block < 32 ? p.block : 32;
   a.NSB = p.N / a.sub;
+  a.shift = 31 - __builtin_clz((unsigned)p.block);
+  a.sub_shift = 31 - __builtin_clz((unsigned)a.sub);
   const long long rts = ((long long)Q * a.G + kRows - 1) / kRows;
   if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
   a.RT = (int)rts;

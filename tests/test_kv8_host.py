@@ -138,11 +138,11 @@ def test_binding_rejects_host_tensors_and_unknown_names():
         bd.rope_params(128, 64, layout="spiral")
     with pytest.raises(ValueError, match="act"):
         bd.kv8_params(8, 2, 64, 16, 64, "f16")
-    dev = torch.device("cpu")
+    dev = -1   # what a CPU tensor says its device index is
     for t, kw, msg in ((torch.zeros(2), dict(dtype=torch.int32), "int32"),
                        (torch.zeros(2), dict(shape=(3,)), "shape"),
                        (torch.zeros(4)[::2], dict(), "contiguous"),
-                       (torch.zeros(2), dict(dev=torch.device("meta")), "on cpu")):
+                       (torch.zeros(2), dict(dev=0), "on cpu")):
         a = dict(dict(dtype=torch.float32, shape=(2,), what="x", dev=dev), **kw)
         with pytest.raises(ValueError, match=msg):
             bd._dense(t, **a)
