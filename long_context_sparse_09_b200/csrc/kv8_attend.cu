@@ -22,16 +22,12 @@
 // mma.sync m16n8k16: at 16 rows a head the loop needs about a third of that
 // path's rate to keep up with HBM, and its operands come from registers, where
 // the codes are widened, without a way through shared or tensor memory.
-#include <cuda.h>
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "kv8.h"
-#include "sm100.cuh"
+#include "kv8_attend.cuh"
 
 namespace csa {
 
 using namespace sm100;
+using namespace kv8;
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_rows);
@@ -39,64 +35,16 @@ bool tma_available();
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 16;          // query rows of a CTA
 constexpr int kTile = 32;          // slots of a warp's tile
-constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
-constexpr float kPShift = 11.f;
-constexpr int kMaxPlan = 1024;     // (sequence, row tile) pairs that the line of units holds
 constexpr int kAccThreads = 128;
-constexpr int kMaxGrid = 256;      // CTAs whose pieces the workspace holds (148 SMs)
 
-struct Kv8AttnArgs {
-  const void* q;
-  const int32_t* n_vis;
-  const uint8_t* k_exp;
-  const uint8_t* v_exp;
-  const float* sink;
-  void* out;
-  float* blk_log;   // [B][H][Q G][NSB] log2 of each sub-block's weight sum (not normalised)
-  float* row_log;   // [B][H][Q G] log2 of the row's denominator
-  float* part_o;    // [grid][2][16][d] pieces of heads that several CTAs share
-  float* part_ml;   // [grid][2][16][2] their M and sum
-  int* plan;        // [E + 1] units before each (sequence, row tile)
-  float* acc;
-  unsigned* err;
-  int B, Q, H, G, N, NB, block;
-  int sub, NSB;     // slots of a sub-block: min(block, 32); sub-blocks of N
-  int shift, sub_shift;  // log2 of block and sub
-  int RT, E, planned;
-  float scale2, decay;  // softmax scale times log2(e)
-};
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-__device__ __forceinline__ int clamp_exp(int e) { return min(max(e, -126), 127); }
-
-// four codes (a 32-bit word) -> two fp16 pairs
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <int D, int SPLIT>
 struct Cfg {
   static constexpr int NW = D == 256 ? 4 : 8;            // warps
@@ -109,51 +57,16 @@ struct Cfg {
   static constexpr int qfrag = ring + NW * NS * 2 * kv_bytes;
   static constexpr int merge = qfrag + SPLIT * steps * 32 * 16;
   static constexpr int ml = merge + NW * kRows * (D + 4) * 4;
-  static constexpr int rows = ml + NW * kRows * 8;       // per row: n_vis, exponent of q
+  static constexpr int rows = ml + NW * kRows * 16;      // per row: n_vis, exponent of q
   static constexpr int plan = rows + kRows * 8;          // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
   static constexpr int total = bars + NW * NS * 8 + 16;
 };
 
-// queries of the rows of row tile rt: rows are query * G + head of the group
-__device__ __forceinline__ int tile_max(const Kv8AttnArgs& a, int b, int rt) {
-  const int j0 = rt * kRows / a.G, j1 = min((rt * kRows + kRows - 1) / a.G, a.Q - 1);
-  int n = 0;
-  for (int j = j0; j <= j1; ++j) {
-    const int v = a.n_vis[(int64_t)b * a.Q + j];
-    if (v > a.N) atomicOr(a.err, CSA_DEV_BAD_INDEX);
-    n = max(n, min(v, a.N));
-  }
-  return n;
-}
-
-// CTA c of `grid` takes the units [cut(c), cut(c + 1)) of the line; grid is at
-// most total, so every range holds a unit (the launch may have more CTAs)
-__device__ __forceinline__ long long cut(long long c, long long total, int grid) {
-  return c * total / grid;
-}
-
-// A walk along the line of units; a unit is one tile for every warp.
-struct Cursor {
-  int e, h, local, units, n;  // (sequence, row tile), KV head, unit in it, its units, n_max
-  __device__ __forceinline__ void load(const int* before, const int* nmax) {
-    units = before[e + 1] - before[e];
-    n = nmax[e];
-  }
-  __device__ __forceinline__ void next(const int* before, const int* nmax, int H, int E) {
-    if (++local < units) return;
-    local = 0;
-    if (++h < H) return;
-    h = 0;
-    do { ++e; } while (e < E && before[e + 1] == before[e]);
-    if (e < E) load(before, nmax);
-  }
-};
-
 template <typename T, int D, int SPLIT>
 __global__ void __launch_bounds__(Cfg<D, SPLIT>::threads, 1)
 kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               Kv8AttnArgs a) {
+               AttnArgs a) {
   using C = Cfg<D, SPLIT>;
   constexpr int NT = D / 8;  // output n-tiles
   extern __shared__ uint8_t smem_raw[];
@@ -161,7 +74,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint8_t* ring = sm + C::ring;
   uint4* qfrag = reinterpret_cast<uint4*>(sm + C::qfrag);
   float* mrg = reinterpret_cast<float*>(sm + C::merge);
-  float2* ml = reinterpret_cast<float2*>(sm + C::ml);
+  float4* ml = reinterpret_cast<float4*>(sm + C::ml);
   int2* rowinfo = reinterpret_cast<int2*>(sm + C::rows);
   int* before = reinterpret_cast<int*>(sm + C::plan);
   int* nmax = before + kMaxPlan + 1;
@@ -178,61 +91,10 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
   pdl_wait();
   pdl_trigger();
-  // ---- the line of units (or this CTA's one item)
   long long u0, u1;
-  int e_base = 0;  // (sequence, row tile) of the line's first entry
+  int e_base;
   Cursor cur;
-  if (a.planned) {
-    const int per = (a.E + C::threads - 1) / C::threads;
-    const int e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
-    unsigned mine = 0, all;
-    for (int e = e0; e < e1; ++e) {
-      const int n = tile_max(a, e / a.RT, e % a.RT);
-      nmax[e] = n;
-      mine += (unsigned)((n + C::unit - 1) / C::unit);
-    }
-    unsigned at = block_exclusive_scan(mine, scan_sh, &all);
-    for (int e = e0; e < e1; ++e) {
-      before[e] = (int)at;
-      at += (unsigned)((nmax[e] + C::unit - 1) / C::unit);
-    }
-    if (tid == 0) before[a.E] = (int)all;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int e = tid; e <= a.E; e += C::threads) a.plan[e] = before[e];
-    const long long total = (long long)all * a.H;
-    const int grid = (int)min((long long)gridDim.x, total);
-    if ((int)blockIdx.x >= grid) return;
-    u0 = cut(blockIdx.x, total, grid);
-    u1 = cut(blockIdx.x + 1, total, grid);
-    int lo = 0, hi = a.E;  // the last e with H * before[e] <= u0 that has units
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((long long)before[mid] * a.H <= u0) lo = mid; else hi = mid;
-    }
-    cur.e = lo;
-    cur.load(before, nmax);
-    const int off = (int)(u0 - (long long)before[lo] * a.H);
-    cur.h = off / cur.units;
-    cur.local = off % cur.units;
-  } else {
-    // one item a CTA, all of its units
-    const int e = (int)(blockIdx.x / a.H);
-    if (tid == 0) {
-      const int n = tile_max(a, e / a.RT, e % a.RT);
-      before[0] = 0;
-      before[1] = (n + C::unit - 1) / C::unit;
-      nmax[0] = n;
-    }
-    __syncthreads();
-    e_base = e;
-    cur.e = 0;
-    cur.h = (int)(blockIdx.x % a.H);
-    cur.local = 0;
-    cur.load(before, nmax);
-    u0 = 0;
-    u1 = max(cur.units, 1);  // an item without slots still writes its zeros
-  }
+  if (!begin_line<C::threads>(a, kRows, C::unit, before, nmax, scan_sh, cur, u0, u1, e_base)) return;
   // ---- this warp's loads
   Cursor pre = cur;
   long long up = u0;
@@ -320,7 +182,8 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     __syncthreads();
     const int2 inf0 = rowinfo[g], inf1 = rowinfo[g + 8];
     const int vis[2] = {inf0.x, inf1.x}, qe[2] = {inf0.y, inf1.y};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool wild = false;  // the sum relative to mx, the maximum of x
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -378,9 +241,41 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           }
         }
       }
-      // ---- y = x + ve, running maximum
       float tmax[2] = {-INFINITY, -INFINITY};
       const bool whole = __all_sync(0xffffffffu, min(vis[0], vis[1]) >= s0 + kTile);
+      float half_sum[2][2];  // by half tile
+      if (wild || max(abs(ve[0]), s0 + 16 < cur.n ? abs(ve[1]) : 0) > kTame) {
+        if (!wild) {
+          wild = true;
+          mx[0] = m[0];
+          mx[1] = m[1];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x[4][2], top = mx[r];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float c = a.scale2 * pow2i(clamp_exp(qe[r] + ke[j >> 1]));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              x[j][k] = s0 + 8 * j + 2 * t + k < vis[r] ? s[j][2 * r + k] * c : -INFINITY;
+              top = fmaxf(top, x[j][k]);
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          l[r] *= top > mx[r] ? fast_exp2(mx[r] - top) : 1.f;
+          mx[r] = top;
+          const float sub = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            half_sum[r][hh] = (fast_exp2(x[2 * hh][0] - sub) + fast_exp2(x[2 * hh][1] - sub)) +
+                              (fast_exp2(x[2 * hh + 1][0] - sub) + fast_exp2(x[2 * hh + 1][1] - sub));
+            l[r] += half_sum[r][hh];
+          }
+        }
+      }
+      // ---- y = x + ve, running maximum
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -413,7 +308,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           const float m1 = fmaxf(m[r], tmax[r]);
           const float f = m1 > m[r] ? fast_exp2(m[r] - m1) : 1.f;
           m[r] = m1;
-          l[r] *= f;
+          if (!wild) l[r] *= f;
 #pragma unroll
           for (int i2 = 0; i2 < NT; ++i2) {
             o[i2][2 * r] *= f;
@@ -421,8 +316,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           }
         }
       }
-      // ---- p = 2^(y - m + 11), its sums by half tile
-      float half_sum[2][2];
+      // ---- p = 2^(y - m + 11), its sums
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float sub = m[r] == -INFINITY ? 0.f : m[r] - kPShift;
@@ -436,8 +330,10 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
               s[j][2 * r + k] = fast_exp2(s[j][2 * r + k] - sub);
               sum += s[j][2 * r + k];
             }
-          half_sum[r][hh] = sum;
-          l[r] = fmaf(sum * 0x1p-11f, pow2i(clamp_exp(-ve[hh])), l[r]);
+          if (!wild) {
+            half_sum[r][hh] = sum;
+            l[r] = fmaf(sum * 0x1p-11f, pow2i(clamp_exp(-ve[hh])), l[r]);
+          }
         }
       }
       if (a.blk_log) {
@@ -451,12 +347,12 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           const int rho = rt * kRows + g + 8 * r;
           if (t == 0 && vis[r] > s0) {
             float* dst = a.blk_log + (head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
-            const float base = m[r] - kPShift;
+            const float base = m[r] - kPShift, b0 = wild ? mx[r] : base - ve[0], b1 = wild ? mx[r] : base - ve[1];
             if (a.sub == 32) {
-              dst[0] = log2f(h0 + h1) + (base - ve[0]);
+              dst[0] = log2f(h0 + h1) + b0;
             } else {
-              dst[0] = log2f(h0) + (base - ve[0]);
-              if (vis[r] > s0 + 16) dst[1] = log2f(h1) + (base - ve[1]);
+              dst[0] = log2f(h0) + b0;
+              if (vis[r] > s0 + 16) dst[1] = log2f(h1) + b1;
             }
           }
         }
@@ -539,7 +435,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       float* dst = mrg + (warp * kRows + g + 8 * r) * (D + 4);
-      if (t == 0) ml[warp * kRows + g + 8 * r] = make_float2(m[r], l[r]);
+      if (t == 0) ml[warp * kRows + g + 8 * r] = make_float4(m[r], wild ? mx[r] : m[r], l[r], 0.f);
       // n-tile (hf, w): column 2t is dim 128 hf + (D == 64 ? 8 : 16) 2t + w
       constexpr int CH = D == 64 ? 8 : 16;
 #pragma unroll
@@ -556,25 +452,28 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     {
       constexpr int TPR = C::threads / kRows;  // threads of a row
       const int r = tid / TPR, rho = rt * kRows + r;
-      float M = -INFINITY, L = 0.f, f[C::NW];
-#pragma unroll
-      for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+      float M = -INFINITY, MX = -INFINITY, L = 0.f, f[C::NW];
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) {
-        const float2 v = ml[w * kRows + r];
+        M = fmaxf(M, ml[w * kRows + r].x);
+        MX = fmaxf(MX, ml[w * kRows + r].y);
+      }
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) {
+        const float4 v = ml[w * kRows + r];
         f[w] = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
-        L = fmaf(v.y, f[w], L);
+        L = fmaf(v.z, v.y == -INFINITY ? 0.f : fast_exp2(v.y - MX), L);
       }
       const bool live = rho < a.Q * a.G;
       float inv = 0.f;
       const int j = rho / a.G, hq = h * a.G + rho % a.G;
       if (complete && live) {
-        if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - M);
-        inv = rowinfo[r].x > 0 ? 0x1p-11f / L : 0.f;
-        if (a.row_log && tid % TPR == 0) a.row_log[head * a.Q * a.G + rho] = log2f(L) + M;
+        if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
+        inv = rowinfo[r].x > 0 ? 0x1p-11f / L * fast_exp2(M - MX) : 0.f;
+        if (a.row_log && tid % TPR == 0) a.row_log[head * a.Q * a.G + rho] = log2f(L) + MX;
       }
       const int64_t slot = (int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1);
-      if (!complete && tid % TPR == 0) reinterpret_cast<float2*>(a.part_ml)[slot * kRows + r] = make_float2(M, L);
+      if (!complete && tid % TPR == 0) a.part_ml[slot * kRows + r] = make_float4(M, MX, L, 0.f);
       T* out = reinterpret_cast<T*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * D;
       float* part = a.part_o + (slot * kRows + r) * D;
 #pragma unroll 1
@@ -617,7 +516,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 // Joins the pieces of the heads that several CTAs share; one CTA a row.  Rows
 // of sequences without slots get their zeros here.
 template <typename T>
-__global__ void kv8_combine(Kv8AttnArgs a, int d, int grid) {
+__global__ void kv8_combine(AttnArgs a, int d, int grid) {
   pdl_wait();
   const int r = (int)(blockIdx.x % kRows);
   const int64_t item = blockIdx.x / kRows;
@@ -631,38 +530,36 @@ __global__ void kv8_combine(Kv8AttnArgs a, int d, int grid) {
     for (int c = threadIdx.x; c < d; c += blockDim.x) out[c] = from_f32<T>(0.f);
     return;
   }
-  const long long total = (long long)a.plan[a.E] * a.H;
-  grid = (int)min((long long)grid, total);
-  const long long U0 = (long long)a.plan[e] * a.H + (long long)h * units, U1 = U0 + units;
-  // the CTAs whose ranges hold the item's first and last unit
-  const int c0 = (int)(((U0 + 1) * grid - 1) / total), c1 = (int)((U1 * grid - 1) / total);
+  const Pieces pc(a, e, h, units, grid);
+  const int c0 = pc.c0, c1 = pc.c1;
   if (c0 == c1) return;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  auto slot = [&](int c) {  // a CTA's first segment is piece 0, its last piece 1
-    return (int64_t)c * 2 + (cut(c, total, grid) >= U0 ? 0 : 1);
-  };
-  float M = -INFINITY;
-  for (int c = c0 + (int)threadIdx.x; c <= c1; c += blockDim.x) M = fmaxf(M, ml[slot(c) * kRows + r].x);
-  __shared__ float red[32];
+  float M = -INFINITY, MX = -INFINITY;
+  for (int c = c0 + (int)threadIdx.x; c <= c1; c += blockDim.x) {
+    const float4 v = a.part_ml[pc.slot(c) * kRows + r];
+    M = fmaxf(M, v.x);
+    MX = fmaxf(MX, v.y);
+  }
+  __shared__ float red[32], red2[32];
   M = block_reduce<true>(M, red);
+  MX = block_reduce<true>(MX, red2);
   float L = 0.f, sum = 0.f;
   const bool mine = (int)threadIdx.x < d;
 #pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
-    const int64_t sl = slot(c);
-    const float2 v = ml[sl * kRows + r];
+    const int64_t sl = pc.slot(c);
+    const float4 v = a.part_ml[sl * kRows + r];
     const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
-    L = fmaf(v.y, f, L);
+    L = fmaf(v.z, v.y == -INFINITY ? 0.f : fast_exp2(v.y - MX), L);
     if (mine) sum = fmaf(a.part_o[(sl * kRows + r) * d + threadIdx.x], f, sum);
   }
-  if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - M);
+  if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
   const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-  if (a.row_log && threadIdx.x == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + M;
-  if (mine) out[threadIdx.x] = from_f32<T>(sees ? sum * (0x1p-11f / L) : 0.f);
+  if (a.row_log && threadIdx.x == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
+  if (mine) out[threadIdx.x] = from_f32<T>(sees ? sum * (0x1p-11f / L * fast_exp2(M - MX)) : 0.f);
 }
 
 // acc = decay acc + sum over the KV head's rows of the weight on a block
-__global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(Kv8AttnArgs a, int tiles) {
+__global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(AttnArgs a, int tiles) {
   pdl_wait();
   const int64_t head = blockIdx.x / tiles;
   const int i = (int)(blockIdx.x % tiles) * kAccThreads + threadIdx.x;
@@ -692,21 +589,25 @@ struct Ws {
   size_t plan, part_ml, part_o, row_log, blk_log, total;
 };
 
+// rows a CTA's piece holds
+int piece_rows(const csa_kv8_params& p, int B, int Q) {
+  return kv8_attend_tc_takes(p, B, Q) ? kv8_attend_tc_rows() : kRows;
+}
+
 Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
-  const size_t rows = (size_t)B * Q * p.n_q;
-  const int grid = kMaxGrid;
+  const size_t rows = (size_t)B * Q * p.n_q, pieces = (size_t)kMaxGrid * 2 * piece_rows(p, B, Q);
   Ws w;
   w.plan = 0;
   w.part_ml = w.plan + align_up((kMaxPlan + 1) * 4, 256);
-  w.part_o = w.part_ml + (size_t)grid * 2 * kRows * 8;
-  w.row_log = w.part_o + (size_t)grid * 2 * kRows * p.d * 4;
+  w.part_o = w.part_ml + pieces * 16;
+  w.row_log = w.part_o + pieces * p.d * 4;
   w.blk_log = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
   w.total = w.blk_log + (acc ? align_up(rows * (p.N / (p.block < 32 ? p.block : 32)) * 4, 256) : 0);
   return w;
 }
 
 template <typename T, int D, int SPLIT>
-csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, Kv8AttnArgs& a, cudaStream_t st) {
+csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, cudaStream_t st) {
   using C = Cfg<D, SPLIT>;
   CUtensorMap tmK, tmV;
   const uint64_t slots = (uint64_t)a.B * a.H * a.N;
@@ -748,15 +649,17 @@ size_t kv8_attend_ws_bytes(const csa_kv8_params& p, int B, int Q, bool acc) {
 csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale, const void* q,
                              const int32_t* n_vis, const Kv8Cache& c, const float* sink,
                              void* out, float* acc, float decay, void* ws, cudaStream_t st) {
-  Kv8AttnArgs a = {};
-  a.q = q; a.n_vis = n_vis; a.k_exp = c.k_exp; a.v_exp = c.v_exp; a.sink = sink; a.out = out;
+  AttnArgs a = {};
+  a.q = q; a.n_vis = n_vis; a.kc = c.kc; a.vc = c.vc; a.k_exp = c.k_exp; a.v_exp = c.v_exp; a.sink = sink; a.out = out;
   a.B = B; a.Q = Q; a.H = p.n_kv; a.G = p.n_q / p.n_kv; a.N = p.N;
   a.NB = p.N / p.block; a.block = p.block;
   a.sub = p.block < 32 ? p.block : 32;
   a.NSB = p.N / a.sub;
   a.shift = 31 - __builtin_clz((unsigned)p.block);
   a.sub_shift = 31 - __builtin_clz((unsigned)a.sub);
-  const long long rts = ((long long)Q * a.G + kRows - 1) / kRows;
+  const bool tc = kv8_attend_tc_takes(p, B, Q);
+  const int rows = piece_rows(p, B, Q);
+  const long long rts = ((long long)Q * a.G + rows - 1) / rows;
   if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
   a.RT = (int)rts;
   a.E = (int)(rts * B);
@@ -764,11 +667,10 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   a.decay = decay;
   a.err = device_error_word();
   if (a.err == nullptr) return CSA_ERR_CUDA;
-  if (!tma_available()) return CSA_ERR_CUDA;
   const Ws w = layout(p, B, Q, acc != nullptr);
   char* base = (char*)ws;
   a.plan = (int*)(base + w.plan);
-  a.part_ml = (float*)(base + w.part_ml);
+  a.part_ml = (float4*)(base + w.part_ml);
   a.part_o = (float*)(base + w.part_o);
   if (acc) {
     a.acc = acc;
@@ -776,7 +678,11 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
     a.blk_log = (float*)(base + w.blk_log);
   }
   csa_status r;
-  if (p.act == CSA_F32)
+  if (tc)
+    r = launch_kv8_attend_tc(p, a, st);
+  else if (!tma_available())
+    return CSA_ERR_CUDA;
+  else if (p.act == CSA_F32)
     r = p.d == 64 ? launch_mma<float, 64, 2>(p, c, a, st)
         : p.d == 128 ? launch_mma<float, 128, 2>(p, c, a, st) : launch_mma<float, 256, 2>(p, c, a, st);
   else

@@ -351,6 +351,78 @@ def test_attend_clamps_and_reports_a_length_beyond_the_cache():
     assert torch.equal(*outs)
 
 
+# many query rows a KV head: lengths around tile and block ends, in any order
+def spread_vis(B, Q, N, seed):
+    g = np.random.default_rng(seed)
+    v = g.integers(-3, N + 1, B * Q)
+    v[g.integers(0, B * Q, 6)] = [0, 1, N, 127 % N, 128 % N, 129 % N]
+    return v.tolist()
+
+
+MANY = [
+    # act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc
+    ("bf16", 1, 130, 1, 1, 64, 16, 16, 1, False, True),
+    ("bf16", 2, 65, 4, 2, 128, 16, 144, 2, True, True),
+    ("bf16", 1, 40, 28, 4, 128, 64, 1088, 3, False, True),
+    ("bf16", 3, 33, 16, 1, 64, 32, 2976, 4, True, False),
+    ("bf16", 1, 129, 3, 3, 64, 128, 1408, 5, True, True),
+    ("bf16", 2, 200, 4, 2, 128, 32, 640, 6, False, True),
+    ("f32", 1, 129, 3, 1, 64, 64, 704, 7, True, True),
+    ("f32", 1, 70, 4, 2, 128, 16, 528, 8, False, True),
+    ("bf16", 1, 45, 6, 2, 256, 32, 992, 9, True, True),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[f"{c[0]}-B{c[1]}-Q{c[2]}-h{c[3]}of{c[4]}-d{c[5]}-blk{c[6]}-N{c[7]}" for c in MANY])
+def test_attend_many_rows(case):
+    act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc = case
+    check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 20 + seed, 0.5)
+
+
+def test_attend_one_tile_of_rows_a_cta():
+    """More row tiles than one line of units holds: sequences without slots
+    among them."""
+    B, Q = 1030, 130
+    vis = [(b * 37 + j) % 17 if b % 5 else 0 for b in range(B) for j in range(Q)]
+    check_attend(("bf16", B, Q, 1, 1, 64, 16, 16, vis, True, True), 31)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("Q,N", [(1, 20480), (80, 4096)])
+@pytest.mark.parametrize("kind", ["zeros first", "zeros between", "all zeros", "far apart"])
+def test_attend_value_exponents_far_apart(act, Q, N, kind):
+    """Blocks of zeros carry the least exponent; blocks of unlike size their
+    own.  Logits do not depend on either, so neither may weights."""
+    B, n_q, n_kv, d, block = 1, 4, 2, 64, 16
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    g = torch.Generator().manual_seed(Q + N)
+    codes = (torch.randn(2, B, n_kv, N, d, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    exps = torch.randint(115, 121, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8)
+    NB = N // block
+    zero = {"zeros first": torch.arange(NB) < 3 * NB // 4, "zeros between": torch.arange(NB) % 3 == 1,
+            "all zeros": torch.ones(NB, dtype=torch.bool), "far apart": torch.zeros(NB, dtype=torch.bool)}[kind]
+    codes[1].view(B, n_kv, NB, block, d)[:, :, zero] = 0
+    exps[1][:, :, zero] = 17
+    if kind == "far apart":
+        exps[1] = torch.tensor([17, 70, 127, 190, 246], dtype=torch.uint8)[torch.randint(0, 5, exps[1].shape, generator=g)]
+    q = (torch.randn(B * Q, n_q, d, generator=g) * 2).to(DT[act])
+    vis = torch.full((B * Q,), N - 5, dtype=torch.int32)
+    acc = torch.zeros(B, n_kv, NB, device=DEV)
+    out = torch.empty(B * Q, n_q, d, dtype=DT[act], device=DEV)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, acc=acc)
+    K, V = (kv8.values(codes[i].numpy(), exps[i].numpy(), block) for i in range(2))
+    ref, wref, mag, load = kv8.attend(q.double().numpy(), vis.tolist(), K, V, block, d ** -0.5)
+    rng = load.max()
+    tol = attend_tol(act, d, N, ref, mag, load, rng)
+    # a term 2^11 2^(y - M) in fp16 is off by half its least step, 2^-25, at most where it is
+    # subnormal: 2^-36 of the largest weight times 2^exponent, for each of N slots' codes up to 448
+    top = N * 2.0 ** -36 * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0) if kind == "far apart" else 0.0
+    within(np64(out), ref, tol + top + 1e-36, "out")
+    eps = (2 * d + 16) * U * rng + 8 * U * rng
+    within(np64(acc), wref, (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * wref + 1e-30, "acc")
+
+
 # ------------------------------------------------------------------- evict --
 EVICT = [
     # B, H, d, block, N, n_tok, keep, recent
