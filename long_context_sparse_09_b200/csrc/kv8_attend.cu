@@ -38,6 +38,8 @@ namespace {
 constexpr int kRows = 16;          // query rows of a CTA
 constexpr int kTile = 32;          // slots of a warp's tile
 constexpr int kAccThreads = 128;
+constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
+constexpr float kPShift = 11.f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "

@@ -14,8 +14,6 @@ namespace csa {
 namespace kv8 {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
-constexpr float kPShift = 11.f;
 constexpr int kMaxPlan = 1024;     // (sequence, row tile) pairs that the line of units holds
 constexpr int kMaxGrid = 160;      // CTAs whose pieces the workspace holds (148 SMs)
 // Value exponents within +-kTame: sums relative to the maximum of y neither

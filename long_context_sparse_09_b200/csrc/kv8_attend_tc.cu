@@ -8,15 +8,24 @@
 // A CTA owns 256 query rows of a KV head (rows are query * G + head of the
 // group) as two streams of 128, and walks the slots in tiles of 128:
 //   S_s = Q_s K^T      tcgen05.mma, both operands in shared memory
-//   P_s = 2^(y - M + 11) by stream s's warpgroup, a thread a row: S is read
-//         from TMEM once, P (fp16) goes back over the front half of S
+//   P_s = 2^(y - M + 7) by stream s's warpgroup, a thread a row: S is read
+//         from TMEM for its maximum and again, 32 slots at a time, for P, which
+//         goes back as fp16 over the front half of S (all of S in registers
+//         spills: 2.9 ms instead of 2.2 at the size below)
 //   O_s += P_s V       tcgen05.mma, P from TMEM, V MN-major in shared memory
 // While a stream's softmax runs, the tensor cores work for the other one.  A
 // third warpgroup widens the codes: 16-byte global loads (a tile ahead, in
 // registers) -> fp16 in the 128-byte swizzle layout, K and V tiles alternating
-// in one ring; that costs each CTA a conversion of the tile, 1/256 of its
-// products.  All tiles of the call lie on one line, cut evenly over the SMs;
+// in one ring.  All tiles of the call lie on one line, cut evenly over the SMs;
 // the pieces of items that several CTAs share are joined by kv8_join.
+//
+// What bounds it: a stream's chain of softmax (3,000 cycles a tile), P V and
+// Q K^T (1,060), of which two run against each other; the tensor cores work 44%
+// of the time.  2048 queries of 64 heads over 32K slots of 8 KV heads (d = 128):
+// 2.15 ms, 990 TFLOP/s, 61% of the measured bf16 rate; on mma.sync
+// (kv8_attend.cu) 11.4 ms.  Tiles of 64 slots with two S buffers a stream took
+// 2.56 ms (a product with N = 64 costs as much as one with N = 128), the
+// products issued by the softmax warps themselves 2.6 ms.
 #include "kv8_attend.cuh"
 
 namespace csa {
@@ -28,7 +37,11 @@ namespace {
 
 constexpr int kTcRows = 256;     // query rows of a CTA: two streams of 128
 constexpr int kTcTile = 128;     // slots of a tile
-constexpr int kTcThreads = 512;  // 2 softmax warpgroups, 1 that widens, 1 for the MMA warp
+constexpr int kTcThreads = 416;  // 2 softmax warpgroups, 1 that widens, the MMA warp
+// The maximum may lag by 2^8, so that few tiles rescale O (a 32-row warp does it
+// together): p = 2^(y - M + 7) stays below fp16's 2^16 and keeps 11 bits down
+// to 2^-21 of 2^M.
+constexpr float kTcLazy = 8.f, kTcShift = 7.f;
 constexpr int kJoinRows = 32;    // rows of a join CTA
 
 template <int D>
@@ -43,19 +56,52 @@ struct Tc {
   static constexpr int total = bars + (2 * NS + 8) * 8 + 16;
 };
 
-template <int kRegs> __device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs> __device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+// 16 bytes of codes (not kept in L1), or zeros
+__device__ __forceinline__ uint4 ld_stream_if(bool yes, const uint8_t* p) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "mov.u32 %3, 0;\n\t@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)yes));
+  return v;
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // codes: not kept in L1
-  uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p));
-  return v;
+// two products and sums, two sums an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// 2^z of a pair, z in [-inf, 127): z = n + r with n the nearest integer (Cody and
+// Waite's reduction), 2^r a minimax polynomial of degree 4 on [-1/2, 1/2]
+// (relative error 2.7e-6, a hundredth of p's rounding to fp16), n added to the
+// exponent.  A quarter of the exponentials go this way, beside the special
+// function unit (2.33 -> 2.21 ms at the size above; a half: 2.32)
+__device__ __forceinline__ float2 exp2_poly(float2 z) {
+  const float2 big = make_float2(12582912.f, 12582912.f), neg = make_float2(-12582912.f, -12582912.f);
+  z.x = fmaxf(z.x, -126.f);
+  z.y = fmaxf(z.y, -126.f);
+  const float2 t = add2(z, big), n = add2(t, neg);
+  const float2 r = fma2(n, make_float2(-1.f, -1.f), z);
+  float2 p = fma2(r, make_float2(0.009570102f, 0.009570102f), make_float2(0.05591786f, 0.05591786f));
+  p = fma2(p, r, make_float2(0.24024744f, 0.24024744f));
+  p = fma2(p, r, make_float2(0.6931218f, 0.6931218f));
+  p = fma2(p, r, make_float2(0.9999993f, 0.9999993f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
 
 template <int D>
@@ -73,7 +119,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
   volatile int* abort_sm = reinterpret_cast<volatile int*>(q_full + 8);
   uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(q_full + 8) + 1;
   __shared__ unsigned scan_sh[33];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     *abort_sm = 0;
     for (int i = 0; i < C::NS; ++i) {
@@ -101,7 +147,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_sm;  // S0, S1: columns 0, 128; O0, O1: 256, 256 + D
+  // all 512 columns are this CTA's, so they start at 0: S0, S1 at 0, 128; O0, O1
+  // at 256, 256 + D
+  if (*tmem_sm != 0) *abort_sm = 1;
 
   // every role walks the same segments: the units of the range that belong to
   // one item
@@ -114,30 +162,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 
   if (warp < 8) {
     // -------------------------------------------------- softmax and output --
-    regs_inc<192>();
     const int st = warp >> 2, row = tid & 127;         // stream, row in it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lanes + st * 128, tO = tbase + lanes + 256 + st * D;
+    const uint32_t tS = lanes + st * 128, tO = lanes + 256 + st * D;
     float4* table = reinterpret_cast<float4*>(sm + C::table) + warp * 16;
-    const float qsign = a.scale2 < 0.f ? -1.f : 1.f, ascale = fabsf(a.scale2);
+    // the scale's sign goes into the queries, its power of two into their
+    // exponents, its mantissa into the keys' factors
+    const float qsign = a.scale2 < 0.f ? -1.f : 1.f;
+    const int scale_e = fabsf(a.scale2) < 0x1p-126f ? 0 : (int)(__float_as_uint(fabsf(a.scale2)) >> 23) - 127;
+    const float scale_m = fabsf(a.scale2) * pow2i(clamp_exp(-scale_e));
     int tiles = 0, segment = 0, parity_o = 0;
     bool ok = true;
     for (long long u = u0; u < u1; ++segment) {
       const int count = segment_units(u);
-      const int h = cur.h, b = (cur.e + e_base) / a.RT, rt = (cur.e + e_base) % a.RT;
-      const int local0 = cur.local, n_max = cur.n;
-      const bool complete = count == cur.units;
-      const int64_t head = (int64_t)b * a.H + h;
-      const int64_t rho = (int64_t)rt * kTcRows + st * 128 + row;
-      const bool live = rho < (int64_t)a.Q * a.G;
-      const int j = live ? (int)(rho / a.G) : 0, hq = h * a.G + (int)(rho % a.G);
-      const int64_t qrow = ((int64_t)b * a.Q + j) * a.H * a.G + hq;
+      const int rho = (cur.e + e_base) % a.RT * kTcRows + st * 128 + row;  // (Q G < 2^31)
+      const int head = (cur.e + e_base) / a.RT * a.H + cur.h;             // (B H < 2^31)
+      const int local0 = cur.local;
+      const bool live = rho < a.Q * a.G;
       // rows beyond the last see everything: no tile needs a mask for them
-      const int vis = live ? min(a.n_vis[(int64_t)b * a.Q + j], a.N) : 0x7fffffff;
+      const int vis = live ? min(a.n_vis[(int64_t)(head / a.H) * a.Q + rho / a.G], a.N) : 0x7fffffff;
+      // element of q and out that the row begins with
+      auto row_at = [&]() {
+        return (((int64_t)(head / a.H) * a.Q + rho / a.G) * a.H * a.G + head % a.H * a.G + rho % a.G) * D;
+      };
       float qscale = 1.f;
       if (count > 0) {
         // ---- Q: fp16 times a power of two per row, largest magnitude in [2^14, 2^15)
-        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + qrow * D);
+        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + (live ? row_at() : 0));
         uint4 raw[D / 8];
         uint32_t top = 0;
 #pragma unroll
@@ -152,7 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
           }
         }
         const int qe = top ? max((int)(top >> 23) - 127 - 14, -126) : 0;
-        qscale = pow2i(qe);
+        qscale = pow2i(clamp_exp(qe + scale_e));
         const float f = pow2i(-qe) * qsign;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -171,15 +222,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
       // exponents of the tile's 16-slot groups: lanes 0-7 hold one of each
-      const uint8_t* ke_p = a.k_exp + head * a.NB;
-      const uint8_t* ve_p = a.v_exp + head * a.NB;
       int ke = 127, ve = 127;
       auto fetch = [&](int i) {
         const int s = (local0 + i) * kTcTile + (lane & 7) * 16;
         ke = ve = 127;
-        if (s < n_max) {
-          ke = ke_p[s >> a.shift];
-          ve = ve_p[s >> a.shift];
+        if (s < cur.n) {
+          const int64_t at = (int64_t)head * a.NB + (s >> a.shift);
+          ke = a.k_exp[at];
+          ve = a.v_exp[at];
         }
       };
       if (count > 0) fetch(0);
@@ -188,54 +238,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         const int s0 = (local0 + i) * kTcTile;
         float4* tab = table + (tiles & 1) * 8;
         const int vl = ve - 127;
-        if (lane < 8) tab[lane] = make_float4(ascale * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - 11)), 0.f);
+        if (lane < 8) tab[lane] = make_float4(scale_m * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
         const bool turn = !wild && __any_sync(0xffffffffu, vl < -kTame || vl > kTame);
         __syncwarp();
         if (i + 1 < count) fetch(i + 1);
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[st], tiles & 1, abort_sm))) { ok = false; break; }
         tc_fence_after();
-        float s[kTcTile];
+        if (__any_sync(0xffffffffu, vis < s0 + kTcTile)) {  // masked slots: -inf, back into S
+#pragma unroll 1
+          for (int c = 0; c < kTcTile; c += 16) {
+            float v[16];
+            tmem_ld16(tS + c, v);
+            tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s + c * 32);
-        tmem_wait_ld();
-        // ---- y = x + ve (kept as s, factor and offset), its maximum
-        if (__any_sync(0xffffffffu, vis < s0 + kTcTile)) {
-#pragma unroll
-          for (int k = 0; k < kTcTile; ++k)
-            if (s0 + k >= vis) s[k] = -INFINITY;
+            for (int k = 0; k < 16; ++k)
+              if (s0 + c + k >= vis) v[k] = -INFINITY;
+            tmem_st16(tS + c, v);
+          }
+          tmem_wait_st();
         }
+        // ---- the largest y = x + ve (S is read here and again below: it does not
+        // stay in registers)
         float tm = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float4 t = tab[g];
-          float top = s[16 * g];
+        for (int hh = 0; hh < 2; ++hh) {
+          float v[64];
+          tmem_ld32(tS + hh * 64, v);
+          tmem_ld32(tS + hh * 64 + 32, v + 32);
+          tmem_wait_ld();
 #pragma unroll
-          for (int k = 1; k < 16; ++k) top = fmaxf(top, s[16 * g + k]);
-          tm = fmaxf(tm, fmaf(top, t.x * qscale, t.y));
+          for (int g = 0; g < 4; ++g) {
+            const float4 t = tab[hh * 4 + g];
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = fmaxf(fmaxf(v[16 * g + k], v[16 * g + k + 4]), fmaxf(v[16 * g + k + 8], v[16 * g + k + 12]));
+            tm = fmaxf(tm, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t.x * qscale, t.y));
+          }
         }
         if (turn) {  // from here on the sum has a reference of its own
           wild = true;
           mx = m;
         }
-        if (__any_sync(0xffffffffu, tm > m + kLazy)) {
+        if (__any_sync(0xffffffffu, tm > m + kTcLazy)) {
           const float m1 = fmaxf(m, tm);
           const float f = m1 > m ? fast_exp2(m - m1) : 1.f;
           if (!wild) l *= f;
           if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (S is there: the P V before it is done)
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
-              float v[16];
-              tmem_ld16(tO + c, v);
+              float w[16];
+              tmem_ld16(tO + c, w);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] *= f;
-              tmem_st16(tO + c, v);
+              for (int k = 0; k < 16; ++k) w[k] *= f;
+              tmem_st16(tO + c, w);
             }
           }
           m = m1;
         }
         float* blk = nullptr;
-        if (a.blk_log && live && vis > s0) blk = a.blk_log + (head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
+        if (a.blk_log && live && vis > s0) blk = a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
         if (wild) {
           // value exponents far apart: p may vanish where the sum does not
           float xm = mx;
@@ -268,35 +331,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
             }
           }
         }
-        // ---- p = 2^(y - m + 11), sums by 16 slots
-        const float off = m == -INFINITY ? 0.f : kPShift - m;
-        float held = 0.f;
-#pragma unroll
+        // ---- p = 2^(y - m + 7), sums by 16 slots
+        const float off = m == -INFINITY ? 0.f : kTcShift - m;
+        float ladd = 0.f;
+#pragma unroll 1
         for (int hh = 0; hh < 4; ++hh) {
-          float pk[16];
+          float v[32];
+          tmem_ld32(tS + hh * 32, v);
+          tmem_wait_ld();
+          float pk[16], sums[2];
 #pragma unroll
-          for (int g = 2 * hh; g < 2 * hh + 2; ++g) {
-            const float4 t = tab[g];
-            const float c = t.x * qscale, o = t.y + off;
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int g = 0; g < 2; ++g) {
+            const float4 t = tab[2 * hh + g];
+            const float2 c = make_float2(t.x * qscale, t.x * qscale), o = make_float2(t.y + off, t.y + off);
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              const float p0 = fast_exp2(fmaf(s[16 * g + k], c, o)), p1 = fast_exp2(fmaf(s[16 * g + k + 1], c, o));
-              s4[k & 2] += p0;
-              s4[(k & 2) + 1] += p1;
-              pk[(g & 1) * 8 + k / 2] = __uint_as_float(pack_h2(p0, p1));
+              const float2 z = fma2(make_float2(v[16 * g + k], v[16 * g + k + 1]), c, o);
+              const float2 p = ((k >> 1) % 4 == 3) ? exp2_poly(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
+              s2[(k >> 1) & 1] = add2(s2[(k >> 1) & 1], p);
+              pk[g * 8 + k / 2] = __uint_as_float(pack_h2(p.x, p.y));
             }
-            const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            if (!wild) {
-              l = fmaf(sum, t.z, l);
-              if (blk && s0 + 16 * g < vis) {
-                if (a.sub == 16) blk[g] = log2f(sum) - (off + t.y);
-                else blk[hh] = log2f(held = (g & 1 ? held : 0.f) + sum) - (off + t.y);
-              }
-            }
+            s2[0] = add2(s2[0], s2[1]);
+            sums[g] = s2[0].x + s2[0].y;
+            ladd = fmaf(sums[g], t.z, ladd);
           }
           tmem_st16(tS + hh * 16, pk);
+          if (blk && !wild && s0 + 32 * hh < vis) {
+            const float b0 = off + tab[2 * hh].y, b1 = off + tab[2 * hh + 1].y;
+            const bool both = s0 + 32 * hh + 16 < vis;
+            if (a.sub == 32) {
+              blk[hh] = log2f(sums[0] + (both ? sums[1] : 0.f)) - b0;
+            } else {
+              blk[2 * hh] = log2f(sums[0]) - b0;
+              if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
+            }
+          }
         }
+        if (!wild) l += ladd;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -304,43 +376,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       }
       if (!ok) break;
       // ---- the item's rows, or this CTA's piece of them
+      const bool complete = count == cur.units;
       if (!wild) mx = m;
-      float L = l, inv = 0.f;
+      float inv = 0.f;
       if (complete && live) {
-        if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - mx);
-        if (vis > 0) inv = 0x1p-11f / L * fast_exp2(m - mx);
-        if (a.row_log) a.row_log[head * a.Q * a.G + rho] = log2f(L) + mx;
+        if (a.sink) l += fast_exp2(a.sink[head % a.H * a.G + rho % a.G] * kLog2e - mx);
+        if (vis > 0) inv = 0x1p-7f / l * fast_exp2(m - mx);
+        if (a.row_log) a.row_log[(int64_t)head * a.Q * a.G + rho] = log2f(l) + mx;
       }
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTcRows + st * 128 + row;
-      if (!complete) a.part_ml[slot] = make_float4(m, mx, L, 0.f);
       if (count > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(&o_full[st], parity_o & 1, abort_sm))) break;
         ++parity_o;
         tc_fence_after();
       }
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + qrow * D;
-      float* part = a.part_o + slot * D;
+      if (!complete) {
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTcRows + st * 128 + row;
+        a.part_ml[slot] = make_float4(m, mx, l, 0.f);
+        float* part = a.part_o + slot * D;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        if (count > 0) {
-          tmem_ld32(tO + c, v);
+        for (int c = 0; c < D; c += 16) {
+          float w[16];
+          tmem_ld16(tO + c, w);
           tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(part + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
         }
-        if (!complete) {
+      } else {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (live ? row_at() : 0);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float w[16];
+          if (count > 0) {
+            tmem_ld16(tO + c, w);
+            tmem_wait_ld();
+          }
+          uint32_t o[8];
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(part + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        } else if (live) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = vis > 0 ? v[k + 2 * i] * inv : 0.f, y = vis > 0 ? v[k + 2 * i + 1] * inv : 0.f;
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(x, y);
-              w[i] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 8; ++k) {  // (a row that sees nothing: zeros, whatever O holds)
+            const __nv_bfloat162 h2 = vis > 0 ? __floats2bfloat162_rn(w[2 * k] * inv, w[2 * k + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          if (live) {
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
       }
@@ -349,27 +427,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
     }
   } else if (warp < 12) {
     // ------------------------------------------------------- widen the codes --
-    regs_dec<88>();
-    constexpr int CH = D / 16;             // 16-byte chunks of a slot
-    constexpr int PER = 128 / CH;          // slots a pass
-    constexpr int NP = kTcTile / PER;      // passes
-    const int t = tid & 127, c = t % CH, r0 = t / CH;
-    const int flip = (c >> 2) & 1;         // which of a chunk's two fp16 chunks goes first: no bank conflicts
-    uint4 kr[NP], vr[NP];
+    constexpr int CH = D / 16;                         // 16-byte chunks of a slot
+    constexpr int PER = 128 / CH;                      // slots a pass
+    constexpr int NP = kTcTile / PER;                  // passes
+    // (a row's upper four chunks go to the neighbouring lanes: the two halves of a
+    // tile lie on the same banks, the rows of a pair on different ones)
+    const int t = tid - 256, c = t % CH, first = t / CH ^ (c >> 2);
+    // K and V tiles in turn; a tile's registers are loaded again as soon as it is
+    // in the ring
     Cursor pre = cur;
-    long long up = u0;
-    int64_t base = 0;   // code of the next tile's first slot
-    int left = 0;       // slots of it that a query sees
+    int64_t from = 0;  // of this thread's chunk of the next tile's first slot
+    int left = 0;      // slots of that tile that a query sees
     auto locate = [&]() {
-      base = (((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + (int64_t)pre.local * kTcTile) * D;
-      left = pre.n - pre.local * kTcTile;
+      from = (((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + (int64_t)pre.local * kTcTile + first) * D + c * 16;
+      left = pre.n - pre.local * kTcTile - first;
     };
-    auto load = [&](const uint8_t* codes, uint4 (&r)[NP]) {
+    auto fetch = [&](uint4 (&r)[NP], const uint8_t* codes) {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int slot = p * PER + r0;
-        r[p] = slot < left ? ld_stream(codes + base + (int64_t)slot * D + c * 16) : make_uint4(0, 0, 0, 0);
-      }
+      for (int p = 0; p < NP; ++p) r[p] = ld_stream_if(p * PER < left, codes + from + p * PER * D);
     };
     int at = 0;  // tiles written to the ring
     auto put = [&](const uint4 (&r)[NP]) -> bool {
@@ -378,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       uint8_t* dst = ring + s * C::row_tile + (c >> 2) * 16384;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const int slot = p * PER + r0;
+        const int slot = p * PER + first;
         uint4 w[2];
         widen4(r[p].x, w[0].x, w[0].y);
         widen4(r[p].y, w[0].z, w[0].w);
@@ -386,8 +461,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         widen4(r[p].w, w[1].z, w[1].w);
         uint8_t* line = dst + slot * 128;
         const int c0 = 2 * (c & 3);
-        *reinterpret_cast<uint4*>(line + (((c0 + flip) ^ (slot & 7)) << 4)) = flip ? w[1] : w[0];
-        *reinterpret_cast<uint4*>(line + (((c0 + 1 - flip) ^ (slot & 7)) << 4)) = flip ? w[0] : w[1];
+        *reinterpret_cast<uint4*>(line + ((c0 ^ (slot & 7)) << 4)) = w[0];
+        *reinterpret_cast<uint4*>(line + (((c0 + 1) ^ (slot & 7)) << 4)) = w[1];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -396,77 +471,92 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       return true;
     };
     if (pre.units > 0) {
-      locate();
-      load(a.kc, kr);
-      while (up < u1) {
-        load(a.vc, vr);
-        if (!put(kr)) break;
+      long long up = u0;   // unit whose tiles are fetched next
+      auto step = [&]() {  // to the next unit; none: nothing is loaded
         if (++up < u1) {
           pre.next(before, nmax, a.H, a.E);
           locate();
-          load(a.kc, kr);
+        } else {
+          left = 0;
         }
-        if (!put(vr)) break;
+      };
+      uint4 k0[NP], v0[NP];
+      locate();
+      fetch(k0, a.kc);
+      fetch(v0, a.vc);
+      step();
+      for (long long u = u0; u < u1; ++u) {
+        if (!put(k0)) break;
+        fetch(k0, a.kc);
+        if (!put(v0)) break;
+        fetch(v0, a.vc);
+        step();
       }
     }
   } else {
-    regs_dec<40>();
-    if (warp == 12 && lane == 0) {
-      // ------------------------------------------------------------- MMA --
-      const uint32_t idesc_qk = idesc_f16(128, kTcTile), idesc_pv = idesc_f16(128, D, true);
-      const uint32_t qb = smem_u32(sQ), rb = smem_u32(ring);
-      int kv = 0, tiles = 0, segs = 0;  // ring tiles and tiles of each stream so far; segments with tiles
-      bool ok = true;
-      auto wait_kv = [&](int i) { return mbar_wait(&kv_full[i % C::NS], (i / C::NS) & 1, abort_sm); };
-      auto issue_qk = [&](int s, int i) {  // S_s = Q_s K^T, K in ring tile i
-        const uint32_t kb = rb + (i % C::NS) * C::row_tile;
+    // --------------------------------------------------------------- MMA --
+    // The whole warp walks the loop on warp-uniform values and one elected lane
+    // issues: descriptors stay in uniform registers (a branch on the lane costs
+    // 75 cycles a product to issue, which the tensor cores do in 64).
+    constexpr uint32_t idesc_qk = idesc_f16(128, kTcTile), idesc_pv = idesc_f16(128, D, true);
+    const uint32_t qb = smem_u32(sQ), rb = smem_u32(ring);
+    int kv = 0, tiles = 0, segs = 0;  // ring tiles and tiles of each stream so far; segments with tiles
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_sm));
+      return ok;
+    };
+    auto wait_kv = [&](int i) { return wait(&kv_full[i % C::NS], (i / C::NS) & 1); };
+    auto issue_qk = [&](int s, int i) {  // S_s = Q_s K^T, K in ring tile i
+      const uint64_t qd = sdesc_k_sw128(qb + s * C::row_tile), kd = sdesc_k_sw128(rb + (i % C::NS) * C::row_tile);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16(tbase + s * 128, sdesc_k_sw128(qb + s * C::row_tile + (k >> 2) * 16384 + (k & 3) * 32),
-                   sdesc_k_sw128(kb + (k >> 2) * 16384 + (k & 3) * 32), idesc_qk, k > 0);
-        mma_commit(&s_full[s]);
-      };
-      for (long long u = u0; ok && u < u1;) {
-        const int count = segment_units(u);
-        if (count > 0) {
-          ok = wait_kv(kv);
-          for (int s = 0; ok && s < 2; ++s) {
-            ok = mbar_wait(&q_full[s], segs & 1, abort_sm);
-            tc_fence_after();
-            if (ok) issue_qk(s, kv);
-          }
-          if (ok) mma_commit(&kv_empty[kv % C::NS]);
-          ++segs;
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t step = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;  // (the address field does not overflow)
+          mma_bf16(s * 128, qd + step, kd + step, idesc_qk, k > 0);
         }
-        for (int i = 0; ok && i < count; ++i, ++tiles, kv += 2) {
-          const uint32_t vb = rb + ((kv + 1) % C::NS) * C::row_tile;
-          for (int s = 0; ok && s < 2; ++s) {
-            if (s == 0) ok = wait_kv(kv + 1);
-            ok = ok && mbar_wait(&p_full[s], tiles & 1, abort_sm);
-            if (!ok) break;
-            tc_fence_after();
+        mma_commit(&s_full[s]);
+        if (s == 1) mma_commit(&kv_empty[i % C::NS]);
+      }
+      __syncwarp();
+    };
+    for (long long u = u0; ok && u < u1;) {
+      const int count = __shfl_sync(0xffffffffu, segment_units(u), 0);
+      if (count > 0) {
+        wait_kv(kv);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!wait(&q_full[s], segs & 1)) break;
+          tc_fence_after();
+          issue_qk(s, kv);
+        }
+        ++segs;
+      }
+#pragma unroll 1
+      for (int i = 0; ok && i < count; ++i, ++tiles, kv += 2) {
+        const uint64_t vd = sdesc_mn_sw128(rb + ((kv + 1) % C::NS) * C::row_tile, 16384, 1024);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s == 0) wait_kv(kv + 1);
+          if (!wait(&p_full[s], tiles & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kTcTile / 16; ++k)
-              mma_f16_ts(tbase + 256 + s * D, tbase + s * 128 + k * 8, sdesc_mn_sw128(vb + k * 2048, 16384, 1024),
-                         idesc_pv, i > 0 || k > 0);
+              mma_f16_ts(256 + s * D, s * 128 + k * 8, vd + k * (2048 >> 4), idesc_pv, i > 0 || k > 0);
             if (s == 1) mma_commit(&kv_empty[(kv + 1) % C::NS]);
-            if (i + 1 < count) {
-              if (s == 0) {
-                ok = wait_kv(kv + 2);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              issue_qk(s, kv + 2);
-              if (s == 1) mma_commit(&kv_empty[(kv + 2) % C::NS]);
-            } else {
-              mma_commit(&o_full[s]);
-            }
+            if (i + 1 == count) mma_commit(&o_full[s]);
+          }
+          __syncwarp();
+          if (i + 1 < count) {
+            if (s == 0 && !wait_kv(kv + 2)) break;
+            tc_fence_after();
+            issue_qk(s, kv + 2);
           }
         }
-        next_segment(u, count);
       }
+      next_segment(u, count);
     }
-    __syncwarp();
   }
   if (*abort_sm && lane == 0) {
     atomicOr(a.err, CSA_DEV_TIMEOUT);
@@ -477,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tbase, 512);
+  if (warp == 12) tmem_dealloc(*tmem_sm, 512);
 }
 
 // Joins the pieces of the items that several CTAs share, a warp a row; rows of
@@ -521,7 +611,7 @@ __global__ void __launch_bounds__(256) kv8_join(AttnArgs a, int launched) {
       if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
       if (a.row_log && lane == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
       const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-      const float inv = 0x1p-11f / L * fast_exp2(M - MX);
+      const float inv = 0x1p-7f / L * fast_exp2(M - MX);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) v[i] = sees ? v[i] * inv : 0.f;
     }
@@ -544,7 +634,9 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
     grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = units;
   }
-  if (items * (kTcRows / kJoinRows) > 0x7fffffffll) return CSA_ERR_SHAPE;
+  if (items * (kTcRows / kJoinRows) > 0x7fffffffll || (long long)a.Q * a.G + kTcRows > 0x7fffffffll ||
+      (long long)a.B * a.H > 0x7fffffffll)
+    return CSA_ERR_SHAPE;
   csa_status ok = CSA_OK;
   CSA_LAUNCH(KK_KV8_ATTEND, st,
              if (launch_maybe_pdl(true, kern, dim3((unsigned)grid), dim3(kTcThreads), smem, st, a) !=
