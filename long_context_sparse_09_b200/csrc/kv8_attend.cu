@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kRows = 16;          // query rows of a CTA
 constexpr int kTile = 32;          // slots of a warp's tile
-constexpr int kAccThreads = 128;
+constexpr int kAccThreads = 256, kAccRows = 512, kAccFew = 32;
 constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
 constexpr float kPShift = 11.f;
 
@@ -560,40 +560,84 @@ __global__ void kv8_combine(AttnArgs a, int d, int grid) {
   if (mine) out[threadIdx.x] = from_f32<T>(sees ? sum * (0x1p-11f / L * fast_exp2(M - MX)) : 0.f);
 }
 
-// acc = decay acc + sum over the KV head's rows of the weight on a block
-__global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(AttnArgs a, int tiles) {
+// acc = decay acc + sum over the KV head's rows of the weight on a block, in a
+// fixed order.  Few rows (decode): a warp sums 32 sub-blocks over all of them.
+// Many: the 8 warps of a CTA share 32 sub-blocks, a row each at a time (128 bytes
+// of blk_log), over at most kAccRows rows; the sums of several such parts go
+// through the workspace (-1: no row sees the block) and kv8_acc_join adds them
+// up.  blk_log is read once, which bounds it where there are many rows.
+template <bool FEW>
+__global__ void __launch_bounds__(kAccThreads) kv8_acc_kernel(AttnArgs a, int tiles, int parts, float* part) {
   pdl_wait();
-  const int64_t head = blockIdx.x / tiles;
-  const int i = (int)(blockIdx.x % tiles) * kAccThreads + threadIdx.x;
-  if (i >= a.NB) return;
-  const int b = (int)(head / a.H), per = a.block / a.sub;
+  constexpr int W = kAccThreads / 32;
+  __shared__ float red[W][33];
+  const int tile = (int)(blockIdx.x % tiles), pt = (int)(blockIdx.x / tiles % parts);
+  const int64_t head = blockIdx.x / tiles / parts;
+  const int b = (int)(head / a.H), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sb = (FEW ? tile * W + warp : tile) * 32 + lane, slot = sb * a.sub;  // sub-block, its first slot
+  const int rows = a.Q * a.G, r1 = min(rows, (pt + 1) * kAccRows);
   float sum = 0.f;
   bool seen = false;
-  for (int j = 0; j < a.Q; ++j) {
-    const int n = min(a.n_vis[(int64_t)b * a.Q + j], a.N);
-    const int left = n - i * a.block;  // slots of the block that the query sees
-    if (left <= 0) continue;
-    seen = true;
-    const int subs = min(per, (left + a.sub - 1) / a.sub);
-    for (int g = 0; g < a.G; ++g) {
-      const int64_t lrow = (head * a.Q + j) * a.G + g;
-      const float den = a.row_log[lrow];
-      for (int k = 0; k < subs; ++k)
-        sum += fast_exp2(a.blk_log[lrow * a.NSB + (int64_t)i * per + k] - den);
+#pragma unroll 4
+  for (int r = pt * kAccRows + (FEW ? 0 : warp); r < r1; r += FEW ? 1 : W) {
+    const int n = min(a.n_vis[(int64_t)b * a.Q + r / a.G], a.N);
+    const int64_t lrow = head * rows + r;
+    if (slot < n) {
+      sum += fast_exp2(a.blk_log[lrow * a.NSB + sb] - a.row_log[lrow]);
+      seen = true;
     }
   }
-  if (!seen) return;
-  float* acc = a.acc + head * a.NB + i;
-  *acc = a.decay == 0.f ? sum : fmaf(a.decay, *acc, sum);
+  if constexpr (!FEW) {
+    red[warp][lane] = seen ? sum : -1.f;
+    __syncthreads();
+    if (warp > 0) return;
+    sum = 0.f;
+    seen = false;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float v = red[w][lane];
+      seen |= v != -1.f;
+      sum += v != -1.f ? v : 0.f;
+    }
+  }
+  const int per = a.block / a.sub;  // 1, 2 or 4 lanes a block
+  for (int o = 1; o < per; o <<= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    seen |= __shfl_xor_sync(0xffffffffu, (int)seen, o) != 0;
+  }
+  if (lane % per != 0 || sb >= a.NSB) return;
+  const int64_t at = head * a.NB + sb / per;
+  if (parts > 1)
+    part[pt * ((int64_t)a.B * a.H * a.NB) + at] = seen ? sum : -1.f;
+  else if (seen)
+    a.acc[at] = a.decay == 0.f ? sum : fmaf(a.decay, a.acc[at], sum);
+}
+__global__ void __launch_bounds__(kAccThreads) kv8_acc_join(AttnArgs a, int parts, const float* part) {
+  pdl_wait();
+  const int64_t n = (int64_t)a.B * a.H * a.NB, at = (int64_t)blockIdx.x * kAccThreads + threadIdx.x;
+  if (at >= n) return;
+  float sum = 0.f;
+  bool seen = false;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float v = part[p * n + at];
+    seen |= v != -1.f;
+    sum += v != -1.f ? v : 0.f;
+  }
+  if (seen) a.acc[at] = a.decay == 0.f ? sum : fmaf(a.decay, a.acc[at], sum);
 }
 
 struct Ws {
-  size_t plan, part_ml, part_o, row_log, blk_log, total;
+  size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
 
 // rows a CTA's piece holds
 int piece_rows(const csa_kv8_params& p, int B, int Q) {
   return kv8_attend_tc_takes(p, B, Q) ? kv8_attend_tc_rows() : kRows;
+}
+
+int acc_parts(const csa_kv8_params& p, int Q) {
+  return (int)(((long long)Q * (p.n_q / p.n_kv) + kAccRows - 1) / kAccRows);
 }
 
 Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
@@ -603,7 +647,9 @@ Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
   w.part_ml = w.plan + align_up((kMaxPlan + 1) * 4, 256);
   w.part_o = w.part_ml + pieces * 16;
   w.row_log = w.part_o + pieces * p.d * 4;
-  w.blk_log = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
+  w.acc_part = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
+  const int parts = acc_parts(p, Q);
+  w.blk_log = w.acc_part + (acc && parts > 1 ? align_up((size_t)parts * B * p.n_kv * (p.N / p.block) * 4, 256) : 0);
   w.total = w.blk_log + (acc ? align_up(rows * (p.N / (p.block < 32 ? p.block : 32)) * 4, 256) : 0);
   return w;
 }
@@ -620,10 +666,10 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
   auto kern = kv8_attend_mma<T, D, SPLIT>;
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
-  // one line of units over all SMs; so many row tiles that they fill the
-  // machine anyway: a CTA each
+  // one line of units over all SMs; a CTA each where an item is one unit at
+  // most, or where there are so many row tiles that they fill the machine anyway
   const long long items = (long long)a.E * a.H;
-  a.planned = a.E <= kMaxPlan;
+  a.planned = a.E <= kMaxPlan && a.N > C::unit;
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + C::unit - 1) / C::unit);
@@ -665,6 +711,12 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
   a.RT = (int)rts;
   a.E = (int)(rts * B);
+  const bool few = (long long)Q * a.G <= kAccFew;
+  const int tiles = (a.NSB + (few ? kAccThreads : 32) - 1) / (few ? kAccThreads : 32), parts = acc_parts(p, Q);
+  const long long blocks = (long long)B * a.H * a.NB;
+  if ((long long)Q * a.G > 0x7fffffffll - kAccRows || (long long)B * a.H * tiles * parts > 0x7fffffffll ||
+      blocks > 0x7fffffffll * kAccThreads)
+    return CSA_ERR_SHAPE;
   a.scale2 = scale * kLog2e;
   a.decay = decay;
   a.err = device_error_word();
@@ -692,13 +744,17 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
         : p.d == 128 ? launch_mma<__nv_bfloat16, 128, 1>(p, c, a, st)
                      : launch_mma<__nv_bfloat16, 256, 1>(p, c, a, st);
   if (r != CSA_OK || !acc) return r;
-  const int tiles = (a.NB + kAccThreads - 1) / kAccThreads;
-  if ((long long)B * a.H * tiles > 0x7fffffffll) return CSA_ERR_SHAPE;
+  float* part = (float*)(base + w.acc_part);
   csa_status ok = CSA_OK;
   CSA_LAUNCH(KK_KV8_ACC, st,
-             if (launch_maybe_pdl(true, kv8_acc_kernel, dim3((unsigned)(B * a.H * tiles)),
-                                  dim3(kAccThreads), 0, st, a, tiles) != cudaSuccess)
-               ok = CSA_ERR_CUDA);
+             if (launch_maybe_pdl(true, few ? kv8_acc_kernel<true> : kv8_acc_kernel<false>,
+                                  dim3((unsigned)(B * a.H * tiles * parts)), dim3(kAccThreads), 0, st, a, tiles, parts,
+                                  part) != cudaSuccess) ok = CSA_ERR_CUDA);
+  if (parts > 1)
+    CSA_LAUNCH(KK_KV8_ACC, st,
+               if (launch_maybe_pdl(true, kv8_acc_join, dim3((unsigned)((blocks + kAccThreads - 1) / kAccThreads)),
+                                    dim3(kAccThreads), 0, st, a, parts, (const float*)part) != cudaSuccess)
+                 ok = CSA_ERR_CUDA);
   return ok != CSA_OK ? ok : last_launch_status();
 }
 

@@ -627,7 +627,7 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
   const int smem = Tc<D>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
-  a.planned = a.E <= kMaxPlan;
+  a.planned = a.E <= kMaxPlan && a.N > kTcTile;
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + kTcTile - 1) / kTcTile);

@@ -370,6 +370,8 @@ MANY = [
     ("f32", 1, 129, 3, 1, 64, 64, 704, 7, True, True),
     ("f32", 1, 70, 4, 2, 128, 16, 528, 8, False, True),
     ("bf16", 1, 45, 6, 2, 256, 32, 992, 9, True, True),
+    ("bf16", 2, 300, 8, 2, 64, 64, 576, 10, False, True),
+    ("bf16", 1, 520, 2, 1, 64, 16, 1040, 11, True, True),
 ]
 
 
