@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kRows = 16;          // query rows of a CTA
 constexpr int kTile = 32;          // slots of a warp's tile
-constexpr int kAccThreads = 256, kAccRows = 512, kAccFew = 32;
+constexpr int kJoinThreads = 256;
+constexpr int kAccThreads = 256, kAccRows = 128, kAccFew = 32;
 constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
 constexpr float kPShift = 11.f;
 
@@ -515,49 +516,63 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
 }
 
-// Joins the pieces of the heads that several CTAs share; one CTA a row.  Rows
-// of sequences without slots get their zeros here.
-template <typename T>
-__global__ void kv8_combine(AttnArgs a, int d, int grid) {
+// Joins the pieces of the heads that several CTAs share; one CTA a row, D / 4
+// threads a piece, so that all pieces are under way at once.  Rows of sequences
+// without slots get their zeros here.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_combine(AttnArgs a, int launched) {
   pdl_wait();
-  const int r = (int)(blockIdx.x % kRows);
+  const int r = (int)(blockIdx.x % kRows), tid = threadIdx.x;
   const int64_t item = blockIdx.x / kRows;
   const int e = (int)(item / a.H), h = (int)(item % a.H), b = e / a.RT, rt = e % a.RT;
   const int rho = rt * kRows + r;
   if (rho >= a.Q * a.G) return;
   const int j = rho / a.G, hq = h * a.G + rho % a.G;
-  T* out = reinterpret_cast<T*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * d;
+  T* out = reinterpret_cast<T*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * D;
   const int units = a.plan[e + 1] - a.plan[e];
   if (units == 0) {
-    for (int c = threadIdx.x; c < d; c += blockDim.x) out[c] = from_f32<T>(0.f);
+    for (int c = tid; c < D; c += kJoinThreads) out[c] = from_f32<T>(0.f);
     return;
   }
-  const Pieces pc(a, e, h, units, grid);
-  const int c0 = pc.c0, c1 = pc.c1;
-  if (c0 == c1) return;
-  float M = -INFINITY, MX = -INFINITY;
-  for (int c = c0 + (int)threadIdx.x; c <= c1; c += blockDim.x) {
-    const float4 v = a.part_ml[pc.slot(c) * kRows + r];
-    M = fmaxf(M, v.x);
-    MX = fmaxf(MX, v.y);
+  const Pieces pc(a, e, h, units, launched);
+  const int n = pc.c1 - pc.c0 + 1;  // at most kMaxGrid <= kJoinThreads
+  if (n == 1) return;
+  constexpr int per = D / 4, groups = kJoinThreads / per;
+  __shared__ float red[32], red2[32], weight[kMaxGrid];
+  __shared__ int64_t where[kMaxGrid];
+  __shared__ float4 sums[groups][per];
+  float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+  if (tid < n) {
+    where[tid] = pc.slot(pc.c0 + tid) * kRows + r;
+    ml = a.part_ml[where[tid]];
   }
-  __shared__ float red[32], red2[32];
-  M = block_reduce<true>(M, red);
-  MX = block_reduce<true>(MX, red2);
-  float L = 0.f, sum = 0.f;
-  const bool mine = (int)threadIdx.x < d;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t sl = pc.slot(c);
-    const float4 v = a.part_ml[sl * kRows + r];
-    const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
-    L = fmaf(v.z, v.y == -INFINITY ? 0.f : fast_exp2(v.y - MX), L);
-    if (mine) sum = fmaf(a.part_o[(sl * kRows + r) * d + threadIdx.x], f, sum);
+  const float M = block_reduce<true>(ml.x, red), MX = block_reduce<true>(ml.y, red2);
+  if (tid < n) weight[tid] = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+  __syncthreads();  // (red is free again, too)
+  float L = block_reduce<false>(ml.y == -INFINITY ? 0.f : ml.z * fast_exp2(ml.y - MX), red);
+  const int g = tid / per, c4 = tid % per * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = g; c < n; c += groups) {
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + where[c] * D + c4);
+    const float f = weight[c];
+    sum.x = fmaf(v.x, f, sum.x);
+    sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z);
+    sum.w = fmaf(v.w, f, sum.w);
   }
+  sums[g][tid % per] = sum;
+  __syncthreads();
   if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
+  if (a.row_log && tid == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
   const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-  if (a.row_log && threadIdx.x == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
-  if (mine) out[threadIdx.x] = from_f32<T>(sees ? sum * (0x1p-11f / L * fast_exp2(M - MX)) : 0.f);
+  const float inv = 0x1p-11f / L * fast_exp2(M - MX);
+  for (int c = tid; c < D; c += kJoinThreads) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < groups; ++k) t += reinterpret_cast<const float*>(&sums[k][0])[c];
+    out[c] = from_f32<T>(sees ? t * inv : 0.f);
+  }
 }
 
 // acc = decay acc + sum over the KV head's rows of the weight on a block, in a
@@ -683,8 +698,8 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
                                   tmV, a) != cudaSuccess) ok = CSA_ERR_CUDA);
   if (a.planned)
     CSA_LAUNCH(KK_KV8_COMBINE, st,
-               if (launch_maybe_pdl(true, kv8_combine<T>, dim3((unsigned)(items * kRows)), dim3(D), 0,
-                                    st, a, D, (int)grid) != cudaSuccess) ok = CSA_ERR_CUDA);
+               if (launch_maybe_pdl(true, kv8_combine<T, D>, dim3((unsigned)(items * kRows)),
+                                    dim3(kJoinThreads), 0, st, a, (int)grid) != cudaSuccess) ok = CSA_ERR_CUDA);
   return ok != CSA_OK ? ok : last_launch_status();
 }
 

@@ -66,13 +66,14 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// the last slot that a query of row tile rt sees, plus one; rows are query * G
-// + head of the group, `rows` of them a tile
-__device__ __forceinline__ int tile_max(const AttnArgs& a, int b, int rt, int rows) {
+// the last slot that queries of row tile rt see, plus one, over every `step`-th
+// of them from `first` on; rows are query * G + head of the group, `rows` a tile
+__device__ __forceinline__ int tile_max(const AttnArgs& a, int b, int rt, int rows, int first, int step) {
   const int j0 = (int)((int64_t)rt * rows / a.G);
   const int j1 = (int)min(((int64_t)rt * rows + rows - 1) / a.G, (int64_t)a.Q - 1);
   int n = 0;
-  for (int j = j0; j <= j1; ++j) {
+#pragma unroll 4
+  for (int j = j0 + first; j <= j1; j += step) {
     const int v = a.n_vis[(int64_t)b * a.Q + j];
     if (v > a.N) atomicOr(a.err, CSA_DEV_BAD_INDEX);
     n = max(n, min(v, a.N));
@@ -115,14 +116,20 @@ __device__ __forceinline__ bool begin_line(const AttnArgs& a, int rows, int unit
   const int tid = threadIdx.x;
   e_base = 0;
   if (a.planned) {
+    // so many lanes an entry that each has about four queries to look at
+    int lpe = 1;
+    while (lpe * 4 < rows / a.G + 1 && lpe < 32) lpe <<= 1;
+    for (int first = 0; first < a.E; first += THREADS / lpe) {
+      const int e = first + tid / lpe;
+      int n = e < a.E ? tile_max(a, e / a.RT, e % a.RT, rows, tid % lpe, lpe) : 0;
+      for (int o = lpe >> 1; o > 0; o >>= 1) n = max(n, __shfl_xor_sync(0xffffffffu, n, o));
+      if (e < a.E && tid % lpe == 0) nmax[e] = n;
+    }
+    __syncthreads();
     const int per = (a.E + THREADS - 1) / THREADS;
     const int e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
     unsigned mine = 0, all;
-    for (int e = e0; e < e1; ++e) {
-      const int n = tile_max(a, e / a.RT, e % a.RT, rows);
-      nmax[e] = n;
-      mine += (unsigned)((n + unit - 1) / unit);
-    }
+    for (int e = e0; e < e1; ++e) mine += (unsigned)((nmax[e] + unit - 1) / unit);
     unsigned at = block_exclusive_scan(mine, scan_sh, &all);
     for (int e = e0; e < e1; ++e) {
       before[e] = (int)at;
@@ -149,11 +156,13 @@ __device__ __forceinline__ bool begin_line(const AttnArgs& a, int rows, int unit
     cur.local = off % cur.units;
   } else {
     const int e = (int)(blockIdx.x / a.H);
-    if (tid == 0) {
-      const int n = tile_max(a, e / a.RT, e % a.RT, rows);
-      before[0] = 0;
-      before[1] = (n + unit - 1) / unit;
-      nmax[0] = n;
+    if (tid < 32) {
+      const int n = __reduce_max_sync(0xffffffffu, tile_max(a, e / a.RT, e % a.RT, rows, tid, 32));
+      if (tid == 0) {
+        before[0] = 0;
+        before[1] = (n + unit - 1) / unit;
+        nmax[0] = n;
+      }
     }
     __syncthreads();
     e_base = e;

@@ -42,7 +42,7 @@ constexpr int kTcThreads = 416;  // 2 softmax warpgroups, 1 that widens, the MMA
 // together): p = 2^(y - M + 7) stays below fp16's 2^16 and keeps 11 bits down
 // to 2^-21 of 2^M.
 constexpr float kTcLazy = 8.f, kTcShift = 7.f;
-constexpr int kJoinRows = 32;    // rows of a join CTA
+constexpr int kJoinRows = 16;    // rows of a join CTA
 
 template <int D>
 struct Tc {
@@ -570,54 +570,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
   if (warp == 12) tmem_dealloc(*tmem_sm, 512);
 }
 
-// Joins the pieces of the items that several CTAs share, a warp a row; rows of
-// sequences without slots get their zeros here.
+// Joins the pieces of the items that several CTAs share, a warp two rows at a
+// time; rows of sequences without slots get their zeros here.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_join(AttnArgs a, int launched) {
   pdl_wait();
-  constexpr int parts = kTcRows / kJoinRows;
+  constexpr int parts = kTcRows / kJoinRows, U = kJoinRows / 8;
   const int64_t item = blockIdx.x / parts;
   const int e = (int)(item / a.H), h = (int)(item % a.H), b = e / a.RT, rt = e % a.RT;
   const int units = a.plan[e + 1] - a.plan[e], lane = threadIdx.x & 31;
+  const int r0 = (int)(blockIdx.x % parts) * kJoinRows + (threadIdx.x >> 5) * U;
+  float v[U][D / 32];
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[k][i] = 0.f;
   if (units > 0) {
     const Pieces pc(a, e, h, units, launched);
     if (pc.c0 == pc.c1) return;
-  }
-#pragma unroll 1
-  for (int r = (int)(blockIdx.x % parts) * kJoinRows + (threadIdx.x >> 5), k = 0; k < kJoinRows / 8; r += 8, ++k) {
-    const int64_t rho = (int64_t)rt * kTcRows + r;
-    if (rho >= (int64_t)a.Q * a.G) return;
-    const int j = (int)(rho / a.G), hq = h * a.G + (int)(rho % a.G);
-    float v[D / 32];
+    float M[U], MX[U], L[U];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
-    if (units > 0) {
-      const Pieces pc(a, e, h, units, launched);
-      float M = -INFINITY, MX = -INFINITY, L = 0.f;
-      for (int c = pc.c0; c <= pc.c1; ++c) {
-        const float4 p = a.part_ml[pc.slot(c) * kTcRows + r];
-        M = fmaxf(M, p.x);
-        MX = fmaxf(MX, p.y);
-      }
+    for (int k = 0; k < U; ++k) M[k] = MX[k] = -INFINITY, L[k] = 0.f;
 #pragma unroll 2
-      for (int c = pc.c0; c <= pc.c1; ++c) {
-        const int64_t sl = pc.slot(c) * kTcRows + r;
-        const float4 p = a.part_ml[sl];
-        const float f = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M);
-        L = fmaf(p.z, p.y == -INFINITY ? 0.f : fast_exp2(p.y - MX), L);
+    for (int c = pc.c0; c <= pc.c1; ++c) {
+      const float4* p = a.part_ml + pc.slot(c) * kTcRows + r0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[i] = fmaf(a.part_o[sl * D + i * 32 + lane], f, v[i]);
+      for (int k = 0; k < U; ++k) {
+        M[k] = fmaxf(M[k], p[k].x);
+        MX[k] = fmaxf(MX[k], p[k].y);
       }
-      if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
-      if (a.row_log && lane == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
-      const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-      const float inv = 0x1p-7f / L * fast_exp2(M - MX);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[i] = sees ? v[i] * inv : 0.f;
     }
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (((int64_t)b * a.Q + j) * a.H * a.G + hq) * D;
+#pragma unroll 2
+    for (int c = pc.c0; c <= pc.c1; ++c) {
+      const int64_t sl = pc.slot(c) * kTcRows + r0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i]);
+      for (int k = 0; k < U; ++k) {
+        const float4 p = a.part_ml[sl + k];
+        const float f = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M[k]);
+        L[k] = fmaf(p.z, p.y == -INFINITY ? 0.f : fast_exp2(p.y - MX[k]), L[k]);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[k][i] = fmaf(a.part_o[(sl + k) * D + i * 32 + lane], f, v[k][i]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t rho = (int64_t)rt * kTcRows + r0 + k;
+      if (rho >= (int64_t)a.Q * a.G) break;
+      const int j = (int)(rho / a.G);
+      if (a.sink) L[k] += fast_exp2(a.sink[h * a.G + (int)(rho % a.G)] * kLog2e - MX[k]);
+      if (a.row_log && lane == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L[k]) + MX[k];
+      const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
+      const float inv = 0x1p-7f / L[k] * fast_exp2(M[k] - MX[k]);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) v[k][i] = sees ? v[k][i] * inv : 0.f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int64_t rho = (int64_t)rt * kTcRows + r0 + k;
+    if (rho >= (int64_t)a.Q * a.G) return;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                         (((int64_t)b * a.Q + rho / a.G) * a.H * a.G + h * a.G + rho % a.G) * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[k][i]);
   }
 }
 

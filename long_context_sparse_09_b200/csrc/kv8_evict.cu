@@ -109,7 +109,17 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
   const int cand = nb - a.recent;  // blocks that compete for the other places
   int need = a.keep - a.recent;
   uint32_t prefix = 0;
-  if (need > 0) {
+  int excess = 0;  // blocks whose key equals the last one's beyond the `need` that stay
+  if (need > 0 && cand <= kSelThreads) {
+    // one key a thread: the key of the need-th largest bit by bit, a vote of
+    // the CTA each (32 votes take a microsecond, the passes below four)
+    const uint32_t k = tid < cand ? weight_key(acc[tid]) : 0u;
+    for (uint32_t bit = 0x80000000u; bit > 0; bit >>= 1)
+      if (__syncthreads_count(tid < cand && k >= (prefix | bit)) >= need) prefix |= bit;
+    need -= __syncthreads_count(tid < cand && k > prefix);
+    excess = __syncthreads_count(tid < cand && k == prefix) - need;
+  } else if (need > 0) {
+    excess = 1;
     // the key of the need-th largest, 8 bits a pass
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
     }
   }
   // blocks whose key equals the last one's: the first `need` of them stay
-  if (need > 0) {
+  if (excess > 0) {
     for (int i0 = (tid & ~31); i0 < words * 32; i0 += kSelThreads) {
       const int i = i0 + lane;
       const unsigned eq = __ballot_sync(0xffffffffu, i < cand && weight_key(acc[i]) == prefix);
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
     bool s = i >= cand && i < nb;
     if (choose && i < cand) {
       const uint32_t k = weight_key(acc[i]);
-      s = k > prefix || (k == prefix && rank_of(stay, before, i) < need);
+      s = k > prefix || (k == prefix && (excess == 0 || rank_of(stay, before, i) < need));
     }
     const unsigned bits = __ballot_sync(0xffffffffu, s);
     __syncwarp();
