@@ -38,6 +38,9 @@ namespace {
 constexpr int kRows = 16;          // query rows of a CTA
 constexpr int kTile = 32;          // slots of a warp's tile
 constexpr int kJoinThreads = 256;
+// A sequence of 2048 tokens, 2 KV heads (d = 128): one line 14.6 us, a CTA an item
+// (6 units) 20.7; 17 sequences of 2496, 8 KV heads, fp32: 41.2 and 27.7.
+constexpr int kJoinUnits = 4;
 constexpr int kAccThreads = 256, kAccRows = 128, kAccFew = 32;
 constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
 constexpr float kPShift = 11.f;
@@ -50,20 +53,21 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t 
 }
 template <int D, int SPLIT>
 struct Cfg {
-  static constexpr int NW = D == 256 ? 4 : 8;            // warps
+  static constexpr int NW = D == 64 ? 16 : D == 128 ? 12 : 6;  // warps
   static constexpr int threads = NW * 32;
   static constexpr int unit = NW * kTile;                // slots of a unit
   static constexpr int kv_bytes = kTile * D;             // one tile of K or V
-  static constexpr int NS = D == 64 ? 4 : 2;             // tiles in a warp's ring
+  static constexpr int NS = D == 64 ? 3 : 2;             // tiles in a warp's ring
+  static constexpr int warp_ring = NS * 2 * kv_bytes;    // (holds the warp's piece in the end: 16 rows of D + 4)
   static constexpr int steps = D / 16;
   static constexpr int ring = 0;
-  static constexpr int qfrag = ring + NW * NS * 2 * kv_bytes;
-  static constexpr int merge = qfrag + SPLIT * steps * 32 * 16;
-  static constexpr int ml = merge + NW * kRows * (D + 4) * 4;
+  static constexpr int qfrag = ring + NW * warp_ring;
+  static constexpr int ml = qfrag + SPLIT * steps * 32 * 16;
   static constexpr int rows = ml + NW * kRows * 16;      // per row: n_vis, exponent of q
   static constexpr int plan = rows + kRows * 8;          // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
   static constexpr int total = bars + NW * NS * 8 + 16;
+  static_assert(kRows * (D + 4) * 4 <= warp_ring && total + 1024 <= 232448, "shared memory");
 };
 
 template <typename T, int D, int SPLIT>
@@ -76,7 +80,6 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = sm + C::ring;
   uint4* qfrag = reinterpret_cast<uint4*>(sm + C::qfrag);
-  float* mrg = reinterpret_cast<float*>(sm + C::merge);
   float4* ml = reinterpret_cast<float4*>(sm + C::ml);
   int2* rowinfo = reinterpret_cast<int2*>(sm + C::rows);
   int* before = reinterpret_cast<int*>(sm + C::plan);
@@ -98,49 +101,10 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   int e_base;
   Cursor cur;
   if (!begin_line<C::threads>(a, kRows, C::unit, before, nmax, scan_sh, cur, u0, u1, e_base)) return;
-  // ---- this warp's loads
-  Cursor pre = cur;
-  long long up = u0;
-  int issued = 0, used = 0;
-  uint8_t* my_ring = ring + warp * C::NS * 2 * C::kv_bytes;
+  int issued = 0, used = 0;  // tiles of this warp so far
+  uint8_t* my_ring = ring + warp * C::warp_ring;
   uint64_t* my_bars = bars + warp * C::NS;
   const uint64_t policy = l2_evict_first_policy();
-  int pre_s0 = 0, pre_row = 0, pre_left = 0;  // next tile's slot, row of the tensor map, units of the item left
-  auto enter = [&]() {
-    pre_s0 = (pre.local * C::NW + warp) * kTile;
-    const int64_t row = ((int64_t)((pre.e + e_base) / a.RT) * a.H + pre.h) * a.N + pre_s0;
-    pre_row = (int)(D == 64 ? row >> 1 : row);  // d = 64: two slots a 128-byte row
-    pre_left = pre.units - pre.local;
-  };
-  enter();
-  auto advance = [&]() {  // issue the loads of the next unit's tile
-    if (up >= u1) return;
-    if (pre_s0 < pre.n) {
-      if (lane == 0) {
-        const int st = issued % C::NS;
-        uint8_t* dst = my_ring + st * 2 * C::kv_bytes;
-        mbar_expect_tx(&my_bars[st], 2 * C::kv_bytes);
-#pragma unroll
-        for (int hf = 0; hf < (D == 256 ? 2 : 1); ++hf) {
-          tma_load_2d_hint(dst + hf * kTile * 128, &tmK, &my_bars[st], hf * 64, pre_row, policy);
-          tma_load_2d_hint(dst + C::kv_bytes + hf * kTile * 128, &tmV, &my_bars[st], hf * 64, pre_row,
-                           policy);
-        }
-      }
-      ++issued;
-    }
-    if (++up >= u1) return;
-    if (--pre_left > 0) {
-      pre_s0 += C::unit;
-      pre_row += D == 64 ? C::unit / 2 : C::unit;
-    } else {
-      pre.local = pre.units - 1;
-      pre.next(before, nmax, a.H, a.E);
-      enter();
-    }
-  };
-#pragma unroll 1
-  for (int i = 0; i < C::NS; ++i) advance();
 
   long long u = u0;
   int segment = 0;
@@ -150,7 +114,30 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int local0 = cur.local, units = cur.units;
     const int count = (int)min((long long)(units - local0), u1 - u);
     const int64_t head = (int64_t)b * a.H + h;
-    __syncthreads();  // the previous segment's queries and merge area are free
+    fence_proxy_async_smem();  // the previous segment's piece in the ring, before loads go there
+    __syncthreads();           // and its queries are free
+    // ---- this warp's loads: of the segment only (the ring then holds its piece)
+    const int first = (local0 * C::NW + warp) * kTile;  // slot of the warp's first tile
+    const int tiles = cur.n > first ? min(count, (cur.n - first + C::unit - 1) / C::unit) : 0;
+    const int64_t first_row = head * a.N + first;
+    auto load = [&](int i) {
+      if (i >= tiles) return;
+      if (lane == 0) {
+        const int st = issued % C::NS;
+        const int row = (int)(D == 64 ? (first_row + (int64_t)i * C::unit) >> 1  // d = 64: two slots a 128-byte row
+                                      : first_row + (int64_t)i * C::unit);
+        uint8_t* dst = my_ring + st * 2 * C::kv_bytes;
+        mbar_expect_tx(&my_bars[st], 2 * C::kv_bytes);
+#pragma unroll
+        for (int hf = 0; hf < (D == 256 ? 2 : 1); ++hf) {
+          tma_load_2d_hint(dst + hf * kTile * 128, &tmK, &my_bars[st], hf * 64, row, policy);
+          tma_load_2d_hint(dst + C::kv_bytes + hf * kTile * 128, &tmV, &my_bars[st], hf * 64, row, policy);
+        }
+      }
+      ++issued;
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::NS; ++i) load(i);
     for (int r = warp; r < kRows; r += C::NW) {
       const int rho = rt * kRows + r, j = rho / a.G, hq = h * a.G + rho % a.G;
       const bool live = rho < a.Q * a.G;
@@ -196,12 +183,8 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const uint8_t* ve_p = a.v_exp + head * a.NB;
 
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      const int s0 = ((local0 + i) * C::NW + warp) * kTile;
-      if (s0 >= cur.n) {  // beyond the item's last slot
-        advance();
-        continue;
-      }
+    for (int i = 0; i < tiles; ++i) {
+      const int s0 = first + i * C::unit;
       // exponents of the tile's two halves (a tile may end beyond the cache)
       const int i0 = s0 >> a.shift, i1 = min((s0 + 16) >> a.shift, a.NB - 1);
       const int ke[2] = {(int)ke_p[i0] - 127, (int)ke_p[i1] - 127};
@@ -428,7 +411,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       }
       if (lim < kTile) fence_proxy_async_smem();  // the zeros before a later load into the tile
       __syncwarp();  // the tile is read
-      advance();
+      load(i + C::NS);
     }
 
     // ---- the warps' pieces become one
@@ -437,7 +420,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      float* dst = mrg + (warp * kRows + g + 8 * r) * (D + 4);
+      float* dst = reinterpret_cast<float*>(my_ring) + (g + 8 * r) * (D + 4);
       if (t == 0) ml[warp * kRows + g + 8 * r] = make_float4(m[r], wild ? mx[r] : m[r], l[r], 0.f);
       // n-tile (hf, w): column 2t is dim 128 hf + (D == 64 ? 8 : 16) 2t + w
       constexpr int CH = D == 64 ? 8 : 16;
@@ -484,7 +467,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::NW; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(mrg + (w * kRows + r) * (D + 4) + c);
+          const float4 v = *reinterpret_cast<const float4*>(ring + w * C::warp_ring + (r * (D + 4) + c) * 4);
           sum.x = fmaf(v.x, f[w], sum.x);
           sum.y = fmaf(v.y, f[w], sum.y);
           sum.z = fmaf(v.z, f[w], sum.z);
@@ -681,14 +664,13 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
   auto kern = kv8_attend_mma<T, D, SPLIT>;
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
-  // one line of units over all SMs; a CTA each where an item is one unit at
-  // most, or where there are so many row tiles that they fill the machine anyway
   const long long items = (long long)a.E * a.H;
-  a.planned = a.E <= kMaxPlan && a.N > C::unit;
+  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+  a.planned = on_a_line(a, C::unit, sms, kJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + C::unit - 1) / C::unit);
-    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    grid = sms;
     if (units < grid) grid = units;
   }
   if (grid > 0x7fffffffll || items * kRows > 0x7fffffffll) return CSA_ERR_SHAPE;

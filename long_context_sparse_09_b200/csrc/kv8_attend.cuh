@@ -194,6 +194,13 @@ struct Pieces {
   }
 };
 
+// Whether the units of all items go on one line: that evens the CTAs out, but the
+// pieces then need a second kernel, which costs as much as `join` units.
+inline bool on_a_line(const AttnArgs& a, int unit, int sms, int join) {
+  const long long items = (long long)a.E * a.H, per = (a.N + unit - 1) / unit;
+  return a.E <= kMaxPlan && (items + sms - 1) / sms * per > (items * per + sms - 1) / sms + join;
+}
+
 }  // namespace kv8
 
 // many query rows a KV head (kv8_attend_tc.cu)

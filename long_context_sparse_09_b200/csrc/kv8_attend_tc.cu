@@ -43,6 +43,9 @@ constexpr int kTcThreads = 416;  // 2 softmax warpgroups, 1 that widens, the MMA
 // to 2^-21 of 2^M.
 constexpr float kTcLazy = 8.f, kTcShift = 7.f;
 constexpr int kJoinRows = 16;    // rows of a join CTA
+// 524 queries (7 heads a KV head, 2 of them) over 1024 slots: one line 45 us, a
+// CTA an item (8 units) 35; over 2048 slots: 47.4 and 53.6.
+constexpr int kJoinUnits = 8;
 
 template <int D>
 struct Tc {
@@ -642,11 +645,12 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
   const int smem = Tc<D>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
-  a.planned = a.E <= kMaxPlan && a.N > kTcTile;
+  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+  a.planned = on_a_line(a, kTcTile, sms, kJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + kTcTile - 1) / kTcTile);
-    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    grid = sms;
     if (units < grid) grid = units;
   }
   if (items * (kTcRows / kJoinRows) > 0x7fffffffll || (long long)a.Q * a.G + kTcRows > 0x7fffffffll ||
