@@ -629,9 +629,22 @@ struct Ws {
   size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
 
+// Whether the call goes to kv8_attend_tc.cu: a unit of it (256 rows x 128 slots)
+// takes 3.2 us, one of this file's (16 rows x 384 or so slots) 2.4.  64 heads, 8
+// of them KV heads, d = 128: 16 queries in 8 sequences of 16K 175 us there, 341
+// here; 5 queries 172 and 144; 16 queries in one sequence of 1024 31 and 14.6.
+bool takes_tc(const csa_kv8_params& p, int B, int Q) {
+  constexpr int sms = 148;
+  const long long tc = kv8_attend_tc_units(p, B, Q, sms);
+  if (tc == 0) return false;
+  const int unit = p.d == 64 ? Cfg<64, 1>::unit : p.d == 128 ? Cfg<128, 1>::unit : Cfg<256, 1>::unit;
+  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kRows - 1) / kRows * B * p.n_kv;
+  return 4 * tc < 3 * line_units(items, p.N, unit, sms, kJoinUnits);
+}
+
 // rows a CTA's piece holds
 int piece_rows(const csa_kv8_params& p, int B, int Q) {
-  return kv8_attend_tc_takes(p, B, Q) ? kv8_attend_tc_rows() : kRows;
+  return takes_tc(p, B, Q) ? kv8_attend_tc_rows() : kRows;
 }
 
 int acc_parts(const csa_kv8_params& p, int Q) {
@@ -666,7 +679,7 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
   const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = on_a_line(a, C::unit, sms, kJoinUnits);
+  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, C::unit, sms, kJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + C::unit - 1) / C::unit);
@@ -702,7 +715,7 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   a.NSB = p.N / a.sub;
   a.shift = 31 - __builtin_clz((unsigned)p.block);
   a.sub_shift = 31 - __builtin_clz((unsigned)a.sub);
-  const bool tc = kv8_attend_tc_takes(p, B, Q);
+  const bool tc = takes_tc(p, B, Q);
   const int rows = piece_rows(p, B, Q);
   const long long rts = ((long long)Q * a.G + rows - 1) / rows;
   if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;

@@ -196,16 +196,22 @@ struct Pieces {
 
 // Whether the units of all items go on one line: that evens the CTAs out, but the
 // pieces then need a second kernel, which costs as much as `join` units.
-inline bool on_a_line(const AttnArgs& a, int unit, int sms, int join) {
-  const long long items = (long long)a.E * a.H, per = (a.N + unit - 1) / unit;
-  return a.E <= kMaxPlan && (items + sms - 1) / sms * per > (items * per + sms - 1) / sms + join;
+inline bool on_a_line(long long items, int N, int unit, int sms, int join) {
+  const long long per = (N + unit - 1) / unit;
+  return (items + sms - 1) / sms * per > (items * per + sms - 1) / sms + join;
+}
+// and what the longest CTA then takes, in units
+inline long long line_units(long long items, int N, int unit, int sms, int join) {
+  const long long per = (N + unit - 1) / unit;
+  return on_a_line(items, N, unit, sms, join) ? (items * per + sms - 1) / sms + join : (items + sms - 1) / sms * per;
 }
 
 }  // namespace kv8
 
-// many query rows a KV head (kv8_attend_tc.cu)
-bool kv8_attend_tc_takes(const csa_kv8_params& p, int B, int Q);
+// many query rows a KV head (kv8_attend_tc.cu): rows of a CTA, units that the
+// longest CTA takes (0: not for these parameters)
 int kv8_attend_tc_rows();
+long long kv8_attend_tc_units(const csa_kv8_params& p, int B, int Q, int sms);
 csa_status launch_kv8_attend_tc(const csa_kv8_params& p, kv8::AttnArgs& a, cudaStream_t st);
 
 }  // namespace csa

@@ -646,7 +646,7 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
   const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = on_a_line(a, kTcTile, sms, kJoinUnits);
+  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, kTcTile, sms, kJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + kTcTile - 1) / kTcTile);
@@ -669,9 +669,10 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool kv8_attend_tc_takes(const csa_kv8_params& p, int B, int Q) {
-  (void)B;
-  return p.act == CSA_BF16 && p.d <= 128 && (int64_t)Q * (p.n_q / p.n_kv) > 128;
+long long kv8_attend_tc_units(const csa_kv8_params& p, int B, int Q, int sms) {
+  if (p.act != CSA_BF16 || p.d > 128) return 0;
+  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kTcRows - 1) / kTcRows * B * p.n_kv;
+  return line_units(items, p.N, kTcTile, sms, kJoinUnits);
 }
 int kv8_attend_tc_rows() { return kTcRows; }
 
