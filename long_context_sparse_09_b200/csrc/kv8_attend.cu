@@ -629,30 +629,32 @@ struct Ws {
   size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
 
-// Whether the call goes to kv8_attend_tc.cu: a unit of it (256 rows x 128 slots)
-// takes 3.2 us, one of this file's (16 rows x 384 or so slots) 2.4.  64 heads, 8
-// of them KV heads, d = 128: 16 queries in 8 sequences of 16K 175 us there, 341
-// here; 5 queries 172 and 144; 16 queries in one sequence of 1024 31 and 14.6.
-bool takes_tc(const csa_kv8_params& p, int B, int Q) {
+// Which form the call takes, by what the longest CTA would take: a unit of this
+// file (16 rows x 384 or so slots) 2.4 us, of kv8_attend_tc.cu (256 rows x 128)
+// 3.2.  64 heads, 8 of them KV heads, d = 128: 16 queries in 8 sequences of 16K
+// 175 us there, 341 here; 5 queries 172 and 144; 16 queries in one sequence of
+// 1024 31 and 14.6.
+enum Form { kMma, kTc, kTc1 };
+Form form_of(const csa_kv8_params& p, int B, int Q) {
   constexpr int sms = 148;
-  const long long tc = kv8_attend_tc_units(p, B, Q, sms);
-  if (tc == 0) return false;
+  const long long tc = kv8_attend_tc_units(p, B, Q, sms), tc1 = kv8_attend_tc1_units(p, B, Q, sms);
   const int unit = p.d == 64 ? Cfg<64, 1>::unit : p.d == 128 ? Cfg<128, 1>::unit : Cfg<256, 1>::unit;
   const long long items = ((long long)Q * (p.n_q / p.n_kv) + kRows - 1) / kRows * B * p.n_kv;
-  return 4 * tc < 3 * line_units(items, p.N, unit, sms, kJoinUnits);
+  const long long here = line_units(items, p.N, unit, sms, kJoinUnits);
+  if (tc > 0 && 4 * tc < 3 * here) return kTc;
+  if (tc1 > 0 && 4 * tc1 < 3 * here) return kTc1;
+  return kMma;
 }
 
 // rows a CTA's piece holds
-int piece_rows(const csa_kv8_params& p, int B, int Q) {
-  return takes_tc(p, B, Q) ? kv8_attend_tc_rows() : kRows;
-}
+int piece_rows(Form f) { return f == kTc ? kv8_attend_tc_rows() : f == kTc1 ? kv8_attend_tc1_rows() : kRows; }
 
 int acc_parts(const csa_kv8_params& p, int Q) {
   return (int)(((long long)Q * (p.n_q / p.n_kv) + kAccRows - 1) / kAccRows);
 }
 
 Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
-  const size_t rows = (size_t)B * Q * p.n_q, pieces = (size_t)kMaxGrid * 2 * piece_rows(p, B, Q);
+  const size_t rows = (size_t)B * Q * p.n_q, pieces = (size_t)kMaxGrid * 2 * piece_rows(form_of(p, B, Q));
   Ws w;
   w.plan = 0;
   w.part_ml = w.plan + align_up((kMaxPlan + 1) * 4, 256);
@@ -715,8 +717,8 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   a.NSB = p.N / a.sub;
   a.shift = 31 - __builtin_clz((unsigned)p.block);
   a.sub_shift = 31 - __builtin_clz((unsigned)a.sub);
-  const bool tc = takes_tc(p, B, Q);
-  const int rows = piece_rows(p, B, Q);
+  const Form form = form_of(p, B, Q);
+  const int rows = piece_rows(form);
   const long long rts = ((long long)Q * a.G + rows - 1) / rows;
   if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
   a.RT = (int)rts;
@@ -742,8 +744,10 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
     a.blk_log = (float*)(base + w.blk_log);
   }
   csa_status r;
-  if (tc)
+  if (form == kTc)
     r = launch_kv8_attend_tc(p, a, st);
+  else if (form == kTc1)
+    r = launch_kv8_attend_tc1(p, a, st);
   else if (!tma_available())
     return CSA_ERR_CUDA;
   else if (p.act == CSA_F32)

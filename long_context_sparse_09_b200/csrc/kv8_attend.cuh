@@ -208,10 +208,13 @@ inline long long line_units(long long items, int N, int unit, int sms, int join)
 
 }  // namespace kv8
 
-// many query rows a KV head (kv8_attend_tc.cu): rows of a CTA, units that the
-// longest CTA takes (0: not for these parameters)
+// many query rows a KV head (kv8_attend_tc.cu; _tc1.cu: fp32 or d = 256): rows of
+// a CTA, units that the longest CTA takes (0: not for these parameters)
 int kv8_attend_tc_rows();
+int kv8_attend_tc1_rows();
 long long kv8_attend_tc_units(const csa_kv8_params& p, int B, int Q, int sms);
+long long kv8_attend_tc1_units(const csa_kv8_params& p, int B, int Q, int sms);
+csa_status launch_kv8_attend_tc1(const csa_kv8_params& p, kv8::AttnArgs& a, cudaStream_t st);
 csa_status launch_kv8_attend_tc(const csa_kv8_params& p, kv8::AttnArgs& a, cudaStream_t st);
 
 }  // namespace csa

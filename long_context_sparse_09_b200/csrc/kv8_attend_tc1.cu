@@ -1,0 +1,552 @@
+// kv8_attend_tc1.cu -- attention over the 8-bit KV cache for many query rows a
+// KV head, fp32 activations or d = 256, on the 5th-generation tensor cores.
+//
+// The mathematics is that of kv8_attend_tc.cu.  fp32 queries and probabilities
+// are two fp16 terms each, so both products run twice; two streams of 128 rows
+// then fit neither shared nor tensor memory, and O of 256 dims does not either.
+// A CTA owns 128 query rows: its two softmax warpgroups take the tiles of slots
+// in turn (S in two buffers), so that Q K^T of the next tile and the softmax of
+// two tiles overlap.  Both add to one O, so they share its reference M (row by
+// row in shared memory): a warpgroup reads what the other one left, raises it
+// where its tile needs that (and rescales O, after the last P V), and passes it
+// on before it forms P.  Sums stay with their warpgroup until the end.
+//
+// What bounds it: %BOUND%
+#include "kv8_attend_tc.cuh"
+
+namespace csa {
+
+using namespace kv8;
+
+namespace {
+
+constexpr int kTc1Rows = 128;  // query rows of a CTA
+constexpr int kJoinUnits = 8;  // as in kv8_attend_tc.cu
+
+template <typename T, int D>
+struct Tc1 {
+  static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of q and p
+  static constexpr int KT = D == 256 ? 64 : 128;        // slots of a tile
+  static constexpr int NG = KT / 16;
+  static constexpr int q_term = kTc1Rows * D * 2;       // a term of the queries
+  static constexpr int kv_tile = KT * D * 2;            // a K or V tile in fp16
+  static constexpr int NS = D == 64 ? 8 : D == 256 && SPLIT == 2 ? 2 : 4;  // of them in the ring
+  static constexpr int q = 0;
+  static constexpr int ring = SPLIT * q_term;
+  static constexpr int table = ring + NS * kv_tile;     // [8 warps][2][NG] float4
+  static constexpr int ref = table + 8 * 2 * NG * 16;   // [128] M of O
+  static constexpr int pair = ref + kTc1Rows * 4;       // [2][128] a warpgroup's reference of its sum, sum
+  static constexpr int plan = pair + 2 * kTc1Rows * 8;  // units before, n_max: [E + 1], [E]
+  static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
+  static constexpr int total = bars + (2 * NS + 10) * 8 + 16;
+  static_assert(total + 1024 <= 232448, "shared memory");
+  // tensor memory: S of the two buffers (P's first term over their front), O, P's
+  // second term
+  static constexpr int colO = 2 * KT, colP2 = colO + D;
+  static_assert(colP2 + (SPLIT - 1) * KT <= 512, "tensor memory");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs a) {
+  using C = Tc1<T, D>;
+  constexpr int KT = C::KT, SPLIT = C::SPLIT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = sm + C::q;
+  uint8_t* ring = sm + C::ring;
+  float* ref = reinterpret_cast<float*>(sm + C::ref);
+  float2* pair = reinterpret_cast<float2*>(sm + C::pair);
+  int* before = reinterpret_cast<int*>(sm + C::plan);
+  int* nmax = before + kMaxPlan + 1;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::bars);
+  uint64_t *kv_full = bars, *kv_empty = bars + C::NS, *s_full = bars + 2 * C::NS, *p_full = s_full + 2,
+           *pv_done = s_full + 4, *turn = s_full + 6, *q_full = s_full + 8, *fin = s_full + 9;
+  volatile int* abort_sm = reinterpret_cast<volatile int*>(s_full + 10);
+  uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(s_full + 10) + 1;
+  __shared__ unsigned scan_sh[33];
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    *abort_sm = 0;
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
+      mbar_init(&turn[s], 4);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(fin, 8);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  long long u0, u1;
+  int e_base;
+  Cursor cur;
+  if (!begin_line<kTcThreads>(a, kTc1Rows, KT, before, nmax, scan_sh, cur, u0, u1, e_base)) return;
+  if (warp == 12) {
+    tmem_alloc(tmem_sm, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // all 512 columns are this CTA's, so they start at 0
+  if (*tmem_sm != 0) *abort_sm = 1;
+
+  auto segment_units = [&](long long u) { return (int)min((long long)(cur.units - cur.local), u1 - u); };
+  auto next_segment = [&](long long& u, int count) {
+    u += max(count, 1);
+    cur.local += count - 1;
+    if (u < u1) cur.next(before, nmax, a.H, a.E);
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------- softmax and output --
+    const int wg = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = lanes + wg * KT, tP2 = lanes + C::colP2 + wg * (KT / 2), tO = lanes + C::colO;
+    float4* table = reinterpret_cast<float4*>(sm + C::table) + warp * 2 * C::NG;
+    // the scale's sign goes into the queries, its power of two into their
+    // exponents, its mantissa into the keys' factors
+    const float qsign = a.scale2 < 0.f ? -1.f : 1.f;
+    const int scale_e = fabsf(a.scale2) < 0x1p-126f ? 0 : (int)(__float_as_uint(fabsf(a.scale2)) >> 23) - 127;
+    const float scale_m = fabsf(a.scale2) * pow2i(clamp_exp(-scale_e));
+    int tile0 = 0, turns = 0, segs = 0, segment = 0;  // tiles before the segment, of both warpgroups
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_sm)) != 0;
+    };
+    for (long long u = u0; u < u1; ++segment) {
+      const int count = segment_units(u);
+      const int rho = (cur.e + e_base) % a.RT * kTc1Rows + row;  // (Q G < 2^31)
+      const int head = (cur.e + e_base) / a.RT * a.H + cur.h;   // (B H < 2^31)
+      const int local0 = cur.local;
+      const bool live = rho < a.Q * a.G;
+      // rows beyond the last see everything: no tile needs a mask for them
+      const int vis = live ? min(a.n_vis[(int64_t)(head / a.H) * a.Q + rho / a.G], a.N) : 0x7fffffff;
+      auto row_at = [&]() {
+        return (((int64_t)(head / a.H) * a.Q + rho / a.G) * a.H * a.G + head % a.H * a.G + rho % a.G) * D;
+      };
+      float qscale = 1.f;
+      if (count > 0) {
+        // ---- Q: fp16 terms times a power of two per row, largest magnitude in
+        // [2^14, 2^15); a warpgroup writes half of the dims
+        const T* q = reinterpret_cast<const T*>(a.q) + (live ? row_at() : 0);
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 16 / (int)sizeof(T)) {
+          const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (SPLIT == 2) {
+              const uint32_t m0 = w[i] & 0x7fffffffu;
+              if (m0 < 0x7f800000u) top = max(top, m0);  // (infinities and NaN do not count)
+            } else {
+              const uint32_t m0 = (w[i] << 16) & 0x7fff0000u, m1 = w[i] & 0x7fff0000u;
+              if (m0 < 0x7f800000u) top = max(top, m0);
+              if (m1 < 0x7f800000u) top = max(top, m1);
+            }
+          }
+        }
+        const int qe = top ? max((int)(top >> 23) - 127 - 14, -126) : 0;
+        qscale = pow2i(clamp_exp(qe + scale_e));
+        const float f = pow2i(-qe) * qsign;
+#pragma unroll 2
+        for (int c8 = wg * (D / 16); c8 < (wg + 1) * (D / 16); ++c8) {  // 8 dims
+          float x[8];
+          if constexpr (SPLIT == 2) {
+            const float4 v0 = live ? *reinterpret_cast<const float4*>(q + c8 * 8) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v1 = live ? *reinterpret_cast<const float4*>(q + c8 * 8 + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[0] = v0.x; x[1] = v0.y; x[2] = v0.z; x[3] = v0.w;
+            x[4] = v1.x; x[5] = v1.y; x[6] = v1.z; x[7] = v1.w;
+          } else {
+            const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c8 * 8) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[2 * i] = __uint_as_float(w[i] << 16);
+              x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float y0 = x[2 * i] * f, y1 = x[2 * i + 1] * f;
+            hi[i] = pack_h2(y0, y1);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+            lo[i] = pack_h2(y0 - h.x, y1 - h.y);
+          }
+          uint8_t* dst = sQ + (c8 >> 3) * (kTc1Rows * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if constexpr (SPLIT == 2) *reinterpret_cast<uint4*>(dst + C::q_term) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      float m = -INFINITY, mx = -INFINITY, l = 0.f;
+      bool wild = false;
+      // exponents of a tile's 16-slot groups: lanes 0 .. NG - 1 hold one of each
+      int ke = 127, ve = 127;
+      auto fetch = [&](int i) {
+        const int s = (local0 + i) * KT + (lane & (C::NG - 1)) * 16;
+        ke = ve = 127;
+        if (s < cur.n) {
+          const int64_t at = (int64_t)head * a.NB + (s >> a.shift);
+          ke = a.k_exp[at];
+          ve = a.v_exp[at];
+        }
+      };
+      const int mine = (tile0 ^ wg) & 1;  // this warpgroup's first tile of the segment
+      if (mine < count) fetch(mine);
+#pragma unroll 1
+      for (int i = mine; i < count; i += 2) {
+        const int s0 = (local0 + i) * KT, tile = tile0 + i;  // (tile & 1 == wg)
+        float4* tab = table + (tile >> 1 & 1) * C::NG;
+        const int vl = ve - 127;
+        if (lane < C::NG)
+          tab[lane] = make_float4(scale_m * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
+        const bool far = !wild && __any_sync(0xffffffffu, vl < -kTame || vl > kTame);
+        __syncwarp();
+        if (i + 2 < count) fetch(i + 2);
+        if (!wait(&s_full[wg], tile >> 1)) { ok = false; break; }
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, vis < s0 + KT)) {  // masked slots: -inf, back into S
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 16) {
+            float v[16];
+            tmem_ld16(tS + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (s0 + c + k >= vis) v[k] = -INFINITY;
+            tmem_st16(tS + c, v);
+          }
+          tmem_wait_st();
+        }
+        // ---- the largest y = x + ve
+        float tm = -INFINITY;
+#pragma unroll
+        for (int hh = 0; hh < KT / 64; ++hh) {
+          float v[64];
+          tmem_ld32(tS + hh * 64, v);
+          tmem_ld32(tS + hh * 64 + 32, v + 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 t = tab[hh * 4 + g];
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = fmaxf(fmaxf(v[16 * g + k], v[16 * g + k + 4]), fmaxf(v[16 * g + k + 8], v[16 * g + k + 12]));
+            tm = fmaxf(tm, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t.x * qscale, t.y));
+          }
+        }
+        if (far) {  // from here on the sum has a reference of its own
+          wild = true;
+          mx = m;
+        }
+        // ---- the reference that the other warpgroup left with the tile before
+        if (i > 0) {
+          if (!wait(&turn[wg], turns++)) { ok = false; break; }
+          const float m0 = ref[row];
+          if (m0 != m) {  // (m0 > m; m = -inf: l is 0)
+            if (!wild) l *= fast_exp2(m - m0);
+            m = m0;
+          }
+        }
+        if (__any_sync(0xffffffffu, tm > m + kTcLazy)) {
+          const float m1 = fmaxf(m, tm);
+          const float f = m1 > m ? fast_exp2(m - m1) : 1.f;
+          if (!wild) l *= f;
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            // (S of this tile was there, so the P V two before it is done)
+            if (!wait(&pv_done[wg ^ 1], (tile - 1) >> 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float w[16];
+              tmem_ld16(tO + c, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] *= f;
+              tmem_st16(tO + c, w);
+            }
+          }
+          m = m1;
+        }
+        ref[row] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&turn[wg ^ 1]);
+        float* blk = nullptr;
+        if (a.blk_log && live && vis > s0) blk = a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
+        if (wild) {
+          // value exponents far apart: p may vanish where the sum does not
+          float xm = mx;
+#pragma unroll 1
+          for (int g = 0; g < C::NG; ++g) {
+            const float c = tab[g].x * qscale;
+            float v[16];
+            tmem_ld16(tS + g * 16, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (s0 + 16 * g + k < vis) xm = fmaxf(xm, v[k] * c);
+          }
+          l *= xm > mx ? fast_exp2(mx - xm) : 1.f;
+          mx = xm;
+          float held = 0.f;
+#pragma unroll 1
+          for (int g = 0; g < C::NG; ++g) {
+            const float c = tab[g].x * qscale;
+            float v[16], sum = 0.f;
+            tmem_ld16(tS + g * 16, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (s0 + 16 * g + k < vis) sum += fast_exp2(fmaf(v[k], c, -mx));
+            l += sum;
+            if (blk && s0 + 16 * g < vis) {
+              if (a.sub == 16) blk[g] = log2f(sum) + mx;
+              else blk[g >> 1] = log2f(held = (g & 1 ? held : 0.f) + sum) + mx;
+            }
+          }
+        }
+        // ---- p = 2^(y - m + 7), sums by 16 slots
+        const float off = m == -INFINITY ? 0.f : kTcShift - m;
+        float ladd = 0.f;
+#pragma unroll 1
+        for (int hh = 0; hh < KT / 32; ++hh) {
+          float v[32];
+          tmem_ld32(tS + hh * 32, v);
+          tmem_wait_ld();
+          float pk[16], pl[16], sums[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float4 t = tab[2 * hh + g];
+            const float2 c = make_float2(t.x * qscale, t.x * qscale), o = make_float2(t.y + off, t.y + off);
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 z = fma2(make_float2(v[16 * g + k], v[16 * g + k + 1]), c, o);
+              // (the polynomial's 2.7e-6 is too much for two terms of fp16)
+              const float2 p = SPLIT == 1 && (k >> 1) % 4 == 3 ? exp2_poly(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
+              s2[(k >> 1) & 1] = add2(s2[(k >> 1) & 1], p);
+              const uint32_t hi = pack_h2(p.x, p.y);
+              pk[g * 8 + k / 2] = __uint_as_float(hi);
+              if constexpr (SPLIT == 2) {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                pl[g * 8 + k / 2] = __uint_as_float(pack_h2(p.x - h.x, p.y - h.y));
+              }
+            }
+            s2[0] = add2(s2[0], s2[1]);
+            sums[g] = s2[0].x + s2[0].y;
+            ladd = fmaf(sums[g], t.z, ladd);
+          }
+          tmem_st16(tS + hh * 16, pk);
+          if constexpr (SPLIT == 2) tmem_st16(tP2 + hh * 16, pl);
+          if (blk && !wild && s0 + 32 * hh < vis) {
+            const float b0 = off + tab[2 * hh].y, b1 = off + tab[2 * hh + 1].y;
+            const bool both = s0 + 32 * hh + 16 < vis;
+            if (a.sub == 32) {
+              blk[hh] = log2f(sums[0] + (both ? sums[1] : 0.f)) - b0;
+            } else {
+              blk[2 * hh] = log2f(sums[0]) - b0;
+              if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
+            }
+          }
+        }
+        if (!wild) l += ladd;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[wg]);
+      }
+      if (!ok) break;
+      // ---- the two sums become one
+      const bool complete = count == cur.units;
+      if (count > 0) {
+        const int last = tile0 + count - 1;
+        if ((last & 1) != wg) {  // the other warpgroup had the last word on the reference
+          if (!wait(&turn[wg], turns++)) break;
+          const float m0 = ref[row];
+          if (m0 != m) {
+            if (!wild) l *= fast_exp2(m - m0);
+            m = m0;
+          }
+        }
+        if (!wild) mx = m;
+        pair[wg * kTc1Rows + row] = make_float2(mx, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fin);
+        if (!wait(fin, segs++)) break;
+        const float2 other = pair[(wg ^ 1) * kTc1Rows + row];
+        const float top = fmaxf(mx, other.x);
+        // (warpgroup 0's part first in both: the two halves of a row get the same sum)
+        const float l0 = wg == 0 ? l : other.y, l1 = wg == 0 ? other.y : l;
+        const float x0 = wg == 0 ? mx : other.x, x1 = wg == 0 ? other.x : mx;
+        l = (x0 == -INFINITY ? 0.f : l0 * fast_exp2(x0 - top)) + (x1 == -INFINITY ? 0.f : l1 * fast_exp2(x1 - top));
+        mx = top;
+        if (!wait(&pv_done[last & 1], last >> 1)) break;
+        tc_fence_after();
+        tile0 += count;
+      }
+      float inv = 0.f;
+      if (complete && live) {
+        if (a.sink) l += fast_exp2(a.sink[head % a.H * a.G + rho % a.G] * kLog2e - mx);
+        if (vis > 0) inv = 0x1p-7f / l * fast_exp2(m - mx);
+        if (a.row_log && wg == 0) a.row_log[(int64_t)head * a.Q * a.G + rho] = log2f(l) + mx;
+      }
+      // ---- the item's rows, or this CTA's piece of them: half of the dims each
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTc1Rows + row;
+      if (!complete && wg == 0) a.part_ml[slot] = make_float4(m, mx, l, 0.f);
+      float* part = a.part_o + slot * D;
+      T* out = reinterpret_cast<T*>(a.out) + (live ? row_at() : 0);
+#pragma unroll 1
+      for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 16) {
+        float w[16];
+        if (count > 0) {
+          tmem_ld16(tO + c, w);
+          tmem_wait_ld();
+        }
+        if (!complete) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(part + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        } else if (live) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = vis > 0 ? w[k] * inv : 0.f;  // (a row that sees nothing: whatever O holds)
+          if constexpr (SPLIT == 2) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(out + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+          } else {
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(w[2 * k], w[2 * k + 1]);
+              o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      next_segment(u, count);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------- widen the codes --
+    widen_role<D, KT, C::NS>(a, cur, u0, u1, e_base, before, nmax, ring, kv_full, kv_empty, abort_sm);
+  } else {
+    // --------------------------------------------------------------- MMA --
+    // (the whole warp on uniform values, one elected lane issues)
+    constexpr uint32_t idesc_qk = idesc_f16(128, KT), idesc_pv = idesc_f16(128, D, true);
+    const uint32_t qb = smem_u32(sQ), rb = smem_u32(ring);
+    int kv = 0, tile = 0, segs = 0;  // ring tiles, tiles so far; segments with tiles
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_sm));
+      return ok;
+    };
+    auto issue_qk = [&](int i, int buf) {  // S = Q K^T, K in ring tile i
+      if (!wait(&kv_full[i % C::NS], i / C::NS)) return;
+      tc_fence_after();
+      const uint64_t qd = sdesc_k_sw128(qb), kd = sdesc_k_sw128(rb + (i % C::NS) * C::kv_tile);
+      if (elect_one()) {
+#pragma unroll
+        for (int t = 0; t < SPLIT; ++t)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)  // (the address fields do not overflow)
+            mma_bf16(buf * KT, qd + ((t * C::q_term + (k >> 2) * (kTc1Rows * 128) + (k & 3) * 32) >> 4),
+                     kd + (((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), idesc_qk, t > 0 || k > 0);
+        mma_commit(&s_full[buf]);
+        mma_commit(&kv_empty[i % C::NS]);
+      }
+      __syncwarp();
+    };
+    for (long long u = u0; ok && u < u1;) {
+      const int count = __shfl_sync(0xffffffffu, segment_units(u), 0);
+      if (count > 0 && wait(q_full, segs++)) issue_qk(kv, tile & 1);
+#pragma unroll 1
+      for (int i = 0; ok && i < count; ++i, ++tile, kv += 2) {
+        const int buf = tile & 1;
+        if (i + 1 < count) issue_qk(kv + 2, buf ^ 1);
+        if (!wait(&kv_full[(kv + 1) % C::NS], (kv + 1) / C::NS) || !wait(&p_full[buf], tile >> 1)) break;
+        tc_fence_after();
+        const uint64_t vd = sdesc_mn_sw128(rb + ((kv + 1) % C::NS) * C::kv_tile, KT * 128, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k) {
+            mma_f16_ts(C::colO, buf * KT + k * 8, vd + k * (2048 >> 4), idesc_pv, i > 0 || k > 0);
+            if constexpr (SPLIT == 2)
+              mma_f16_ts(C::colO, C::colP2 + buf * (KT / 2) + k * 8, vd + k * (2048 >> 4), idesc_pv, 1);
+          }
+          mma_commit(&pv_done[buf]);
+          mma_commit(&kv_empty[(kv + 1) % C::NS]);
+        }
+        __syncwarp();
+      }
+      next_segment(u, count);
+    }
+  }
+  if (*abort_sm && lane == 0) {
+    atomicOr(a.err, CSA_DEV_TIMEOUT);
+    const uint64_t t0 = globaltimer();  // products already issued end before TMEM is given back
+    while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(*tmem_sm, 512);
+}
+
+template <typename T, int D>
+csa_status launch_tc1(AttnArgs& a, cudaStream_t st) {
+  auto kern = kv8_attend_tc1_kernel<T, D>;
+  const int smem = Tc1<T, D>::total + 1024;
+  if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
+  const long long items = (long long)a.E * a.H;
+  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, Tc1<T, D>::KT, sms, kJoinUnits);
+  long long grid = items;
+  if (a.planned) {
+    const long long units = items * ((a.N + Tc1<T, D>::KT - 1) / Tc1<T, D>::KT);
+    grid = sms;
+    if (units < grid) grid = units;
+  }
+  if (items * (kTc1Rows / kTcJoinRows) > 0x7fffffffll || (long long)a.Q * a.G + kTc1Rows > 0x7fffffffll ||
+      (long long)a.B * a.H > 0x7fffffffll)
+    return CSA_ERR_SHAPE;
+  csa_status ok = CSA_OK;
+  CSA_LAUNCH(KK_KV8_ATTEND, st,
+             if (launch_maybe_pdl(true, kern, dim3((unsigned)grid), dim3(kTcThreads), smem, st, a) !=
+                 cudaSuccess) ok = CSA_ERR_CUDA);
+  if (a.planned)
+    CSA_LAUNCH(KK_KV8_COMBINE, st,
+               if (launch_maybe_pdl(true, (kv8_join<T, D, kTc1Rows>),
+                                    dim3((unsigned)(items * (kTc1Rows / kTcJoinRows))), dim3(256), 0, st, a,
+                                    (int)grid) != cudaSuccess) ok = CSA_ERR_CUDA);
+  return ok != CSA_OK ? ok : last_launch_status();
+}
+
+}  // namespace
+
+long long kv8_attend_tc1_units(const csa_kv8_params& p, int B, int Q, int sms) {
+  if (p.act == CSA_BF16 && p.d <= 128) return 0;
+  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kTc1Rows - 1) / kTc1Rows * B * p.n_kv;
+  return line_units(items, p.N, p.d == 256 ? 64 : 128, sms, kJoinUnits);
+}
+int kv8_attend_tc1_rows() { return kTc1Rows; }
+
+csa_status launch_kv8_attend_tc1(const csa_kv8_params& p, AttnArgs& a, cudaStream_t st) {
+  if (p.act == CSA_F32)
+    return p.d == 64 ? launch_tc1<float, 64>(a, st) : p.d == 128 ? launch_tc1<float, 128>(a, st) : launch_tc1<float, 256>(a, st);
+  return p.d == 256 ? launch_tc1<__nv_bfloat16, 256>(a, st) : CSA_ERR_UNSUPPORTED;
+}
+
+}  // namespace csa

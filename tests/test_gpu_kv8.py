@@ -310,7 +310,7 @@ def test_attend_is_repeatable_bit_for_bit():
     assert torch.equal(a, b) and torch.equal(wa, wb)
 
 
-@pytest.mark.parametrize("Q", [1, 2, 65])
+@pytest.mark.parametrize("Q", [1, 2, 65, 2000])
 def test_attend_extreme_values(Q):
     """Query magnitudes far from 1, block exponents far apart, logits that
     leave one slot, and a slot with a tiny value that takes all weight."""
@@ -381,6 +381,40 @@ def test_attend_many_rows(case):
     check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 20 + seed, 0.5)
 
 
+def rows_of_a_cta(p, B, Q):
+    """Query rows that a CTA of the call owns, from the size of its pieces:
+    16 (mma.sync), 256 or 128 (tcgen05)."""
+    small = bd.kv8_params(p.n_kv, p.n_kv, p.d, p.block, p.block, "bf16")   # one row: 16
+    a, b = bd.kv8_attend_workspace_bytes(p, B, Q, False), bd.kv8_attend_workspace_bytes(small, 1, 1, False)
+    return 16 + (a - b) // (2 * 160 * (16 + 4 * p.d))
+
+
+WIDE = [
+    # rows and KV heads enough for the tensor-core forms: one tile, several, one line of units
+    ("bf16", 2, 70, 64, 4, 64, 16, 48, 1, True, True),
+    ("bf16", 1, 150, 64, 8, 128, 32, 160, 2, False, True),
+    ("bf16", 2, 190, 48, 8, 128, 64, 704, 3, True, False),
+    ("bf16", 1, 1000, 7, 1, 64, 128, 4096, 4, False, True),
+    ("bf16", 1, 290, 14, 1, 128, 16, 4000, 5, True, True),
+    ("f32", 2, 70, 64, 4, 64, 32, 96, 6, True, True),
+    ("f32", 1, 150, 64, 8, 128, 16, 272, 7, False, True),
+    ("f32", 1, 300, 48, 6, 256, 64, 192, 8, True, False),
+    ("f32", 1, 290, 14, 1, 128, 64, 4032, 9, True, True),
+    ("bf16", 1, 150, 64, 8, 256, 16, 144, 10, True, True),
+    ("bf16", 2, 300, 24, 4, 256, 128, 384, 11, False, True),
+    ("bf16", 1, 290, 14, 1, 256, 32, 2016, 12, False, False),
+    ("f32", 1, 290, 14, 1, 256, 16, 2000, 13, False, True),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-B{c[1]}-Q{c[2]}-h{c[3]}of{c[4]}-d{c[5]}-blk{c[6]}-N{c[7]}" for c in WIDE])
+def test_attend_tensor_core_forms(case):
+    act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc = case
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    assert rows_of_a_cta(p, B, Q) == (256 if act == "bf16" and d <= 128 else 128)
+    check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 40 + seed, 0.5)
+
+
 def test_attend_one_tile_of_rows_a_cta():
     """More row tiles than one line of units holds: sequences without slots
     among them."""
@@ -390,13 +424,14 @@ def test_attend_one_tile_of_rows_a_cta():
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("Q,N", [(1, 20480), (80, 4096)])
+@pytest.mark.parametrize("Q,N", [(1, 20480), (80, 4096), (2000, 640)])
 @pytest.mark.parametrize("kind", ["zeros first", "zeros between", "all zeros", "far apart"])
 def test_attend_value_exponents_far_apart(act, Q, N, kind):
     """Blocks of zeros carry the least exponent; blocks of unlike size their
     own.  Logits do not depend on either, so neither may weights."""
     B, n_q, n_kv, d, block = 1, 4, 2, 64, 16
     p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    assert rows_of_a_cta(p, B, Q) == (16 if Q < 2000 else 256 if act == "bf16" else 128)
     g = torch.Generator().manual_seed(Q + N)
     codes = (torch.randn(2, B, n_kv, N, d, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     exps = torch.randint(115, 121, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8)
@@ -419,8 +454,8 @@ def test_attend_value_exponents_far_apart(act, Q, N, kind):
     tol = attend_tol(act, d, N, ref, mag, load, rng)
     # a term 2^7 2^(y - M) in fp16 is off by half its least step, 2^-25, at most where it is
     # subnormal: 2^-32 of the largest weight times 2^exponent, for each of N slots' codes up to 448
-    # (one query: 2^11 2^(y - M), so 2^-36)
-    top = N * 2.0 ** (-36 if Q == 1 else -32) * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0) if kind == "far apart" else 0.0
+    # (few rows a KV head: 2^11 2^(y - M), so 2^-36)
+    top = N * 2.0 ** (-32 if Q == 2000 else -36) * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0) if kind == "far apart" else 0.0
     within(np64(out), ref, tol + top + 1e-36, "out")
     eps = (2 * d + 16) * U * rng + 8 * U * rng
     within(np64(acc), wref, (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * wref + 1e-30, "acc")
