@@ -629,21 +629,32 @@ struct Ws {
   size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
 
-// Which form the call takes, by what the longest CTA would take: a unit of this
-// file (16 rows x 384 or so slots) 2.4 us, of kv8_attend_tc.cu (256 rows x 128)
-// 3.2.  64 heads, 8 of them KV heads, d = 128: 16 queries in 8 sequences of 16K
-// 175 us there, 341 here; 5 queries 172 and 144; 16 queries in one sequence of
-// 1024 31 and 14.6.
+// Which form the call takes: the one whose longest CTA is done first, at the time
+// that a unit takes (measured on long prompts, tenths of a us; the tensor-core
+// forms take 5 us more to set up).  64 heads, 8 of
+// them KV heads, d = 128, bf16, here / two streams / one tile of 128 rows: 8
+// sequences of 16K, 5 queries 144 us / 172 / 109, 16 queries 341 / 175 / -; 8 of
+// 2K, 32 queries - / 64 / 48; one prompt of 32K, the last 2048 queries 11,400 / 2,150 /
+// 2,580.
 enum Form { kMma, kTc, kTc1 };
 Form form_of(const csa_kv8_params& p, int B, int Q) {
   constexpr int sms = 148;
-  const long long tc = kv8_attend_tc_units(p, B, Q, sms), tc1 = kv8_attend_tc1_units(p, B, Q, sms);
+  const bool f32 = p.act == CSA_F32;
+  const long long rows = (long long)Q * (p.n_q / p.n_kv), heads = (long long)B * p.n_kv;
+  auto cost = [&](int tile_rows, int unit, int join, int each) {
+    return each * line_units((rows + tile_rows - 1) / tile_rows * heads, p.N, unit, sms, join);
+  };
   const int unit = p.d == 64 ? Cfg<64, 1>::unit : p.d == 128 ? Cfg<128, 1>::unit : Cfg<256, 1>::unit;
-  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kRows - 1) / kRows * B * p.n_kv;
-  const long long here = line_units(items, p.N, unit, sms, kJoinUnits);
-  if (tc > 0 && 4 * tc < 3 * here) return kTc;
-  if (tc1 > 0 && 4 * tc1 < 3 * here) return kTc1;
-  return kMma;
+  long long best = cost(kRows, unit, kJoinUnits, f32 ? 31 : 24);
+  Form form = kMma;
+  if (rows <= 2 * kRows) return form;
+  if (!f32 && p.d <= 128) {
+    const long long c = 50 + cost(kv8_attend_tc_rows(), 128, kTcJoinUnits, 32);
+    if (c < best) best = c, form = kTc;
+  }
+  const long long c = 50 + cost(kv8_attend_tc1_rows(), p.d == 256 ? 64 : 128, kTcJoinUnits,
+                           p.d == 64 ? 19 : p.d == 128 ? (f32 ? 23 : 19) : (f32 ? 32 : 15));
+  return c < best ? kTc1 : form;
 }
 
 // rows a CTA's piece holds

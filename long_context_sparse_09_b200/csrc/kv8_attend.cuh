@@ -14,6 +14,9 @@ namespace csa {
 namespace kv8 {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// Tensor-core forms: 524 queries (7 heads a KV head, 2 of them, d = 128, bf16) over
+// 1024 slots: one line 45 us, a CTA an item (8 units) 35; over 2048: 47.4 and 53.6.
+constexpr int kTcJoinUnits = 8;
 constexpr int kMaxPlan = 1024;     // (sequence, row tile) pairs that the line of units holds
 constexpr int kMaxGrid = 160;      // CTAs whose pieces the workspace holds (148 SMs)
 // Value exponents within +-kTame: sums relative to the maximum of y neither
@@ -208,12 +211,10 @@ inline long long line_units(long long items, int N, int unit, int sms, int join)
 
 }  // namespace kv8
 
-// many query rows a KV head (kv8_attend_tc.cu; _tc1.cu: fp32 or d = 256): rows of
-// a CTA, units that the longest CTA takes (0: not for these parameters)
+// many query rows a KV head (kv8_attend_tc.cu: bf16, d <= 128; kv8_attend_tc1.cu):
+// rows of a CTA
 int kv8_attend_tc_rows();
 int kv8_attend_tc1_rows();
-long long kv8_attend_tc_units(const csa_kv8_params& p, int B, int Q, int sms);
-long long kv8_attend_tc1_units(const csa_kv8_params& p, int B, int Q, int sms);
 csa_status launch_kv8_attend_tc1(const csa_kv8_params& p, kv8::AttnArgs& a, cudaStream_t st);
 csa_status launch_kv8_attend_tc(const csa_kv8_params& p, kv8::AttnArgs& a, cudaStream_t st);
 

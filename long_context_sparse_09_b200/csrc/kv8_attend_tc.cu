@@ -36,9 +36,6 @@ namespace {
 
 constexpr int kTcRows = 256;     // query rows of a CTA: two streams of 128
 constexpr int kTcTile = 128;     // slots of a tile
-// 524 queries (7 heads a KV head, 2 of them) over 1024 slots: one line 45 us, a
-// CTA an item (8 units) 35; over 2048 slots: 47.4 and 53.6.
-constexpr int kJoinUnits = 8;
 
 template <int D>
 struct Tc {
@@ -460,7 +457,7 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
   const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, kTcTile, sms, kJoinUnits);
+  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, kTcTile, sms, kTcJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + kTcTile - 1) / kTcTile);
@@ -483,11 +480,6 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-long long kv8_attend_tc_units(const csa_kv8_params& p, int B, int Q, int sms) {
-  if (p.act != CSA_BF16 || p.d > 128) return 0;
-  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kTcRows - 1) / kTcRows * B * p.n_kv;
-  return line_units(items, p.N, kTcTile, sms, kJoinUnits);
-}
 int kv8_attend_tc_rows() { return kTcRows; }
 
 csa_status launch_kv8_attend_tc(const csa_kv8_params& p, AttnArgs& a, cudaStream_t st) {

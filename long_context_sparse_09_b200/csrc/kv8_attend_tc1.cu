@@ -1,5 +1,6 @@
 // kv8_attend_tc1.cu -- attention over the 8-bit KV cache for many query rows a
-// KV head, fp32 activations or d = 256, on the 5th-generation tensor cores.
+// KV head, fp32 activations or d = 256 or calls too small for CTAs of 256 rows,
+// on the 5th-generation tensor cores.
 //
 // The mathematics is that of kv8_attend_tc.cu.  fp32 queries and probabilities
 // are two fp16 terms each, so both products run twice; two streams of 128 rows
@@ -21,7 +22,6 @@ using namespace kv8;
 namespace {
 
 constexpr int kTc1Rows = 128;  // query rows of a CTA
-constexpr int kJoinUnits = 8;  // as in kv8_attend_tc.cu
 
 template <typename T, int D>
 struct Tc1 {
@@ -512,7 +512,7 @@ csa_status launch_tc1(AttnArgs& a, cudaStream_t st) {
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
   const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, Tc1<T, D>::KT, sms, kJoinUnits);
+  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, Tc1<T, D>::KT, sms, kTcJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + Tc1<T, D>::KT - 1) / Tc1<T, D>::KT);
@@ -536,17 +536,12 @@ csa_status launch_tc1(AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-long long kv8_attend_tc1_units(const csa_kv8_params& p, int B, int Q, int sms) {
-  if (p.act == CSA_BF16 && p.d <= 128) return 0;
-  const long long items = ((long long)Q * (p.n_q / p.n_kv) + kTc1Rows - 1) / kTc1Rows * B * p.n_kv;
-  return line_units(items, p.N, p.d == 256 ? 64 : 128, sms, kJoinUnits);
-}
 int kv8_attend_tc1_rows() { return kTc1Rows; }
 
 csa_status launch_kv8_attend_tc1(const csa_kv8_params& p, AttnArgs& a, cudaStream_t st) {
   if (p.act == CSA_F32)
     return p.d == 64 ? launch_tc1<float, 64>(a, st) : p.d == 128 ? launch_tc1<float, 128>(a, st) : launch_tc1<float, 256>(a, st);
-  return p.d == 256 ? launch_tc1<__nv_bfloat16, 256>(a, st) : CSA_ERR_UNSUPPORTED;
+  return p.d == 64 ? launch_tc1<__nv_bfloat16, 64>(a, st) : p.d == 128 ? launch_tc1<__nv_bfloat16, 128>(a, st) : launch_tc1<__nv_bfloat16, 256>(a, st);
 }
 
 }  // namespace csa

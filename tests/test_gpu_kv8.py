@@ -390,29 +390,51 @@ def rows_of_a_cta(p, B, Q):
 
 
 WIDE = [
-    # rows and KV heads enough for the tensor-core forms: one tile, several, one line of units
-    ("bf16", 2, 70, 64, 4, 64, 16, 48, 1, True, True),
-    ("bf16", 1, 150, 64, 8, 128, 32, 160, 2, False, True),
-    ("bf16", 2, 190, 48, 8, 128, 64, 704, 3, True, False),
-    ("bf16", 1, 1000, 7, 1, 64, 128, 4096, 4, False, True),
-    ("bf16", 1, 290, 14, 1, 128, 16, 4000, 5, True, True),
-    ("f32", 2, 70, 64, 4, 64, 32, 96, 6, True, True),
-    ("f32", 1, 150, 64, 8, 128, 16, 272, 7, False, True),
-    ("f32", 1, 300, 48, 6, 256, 64, 192, 8, True, False),
-    ("f32", 1, 290, 14, 1, 128, 64, 4032, 9, True, True),
-    ("bf16", 1, 150, 64, 8, 256, 16, 144, 10, True, True),
-    ("bf16", 2, 300, 24, 4, 256, 128, 384, 11, False, True),
-    ("bf16", 1, 290, 14, 1, 256, 32, 2016, 12, False, False),
-    ("f32", 1, 290, 14, 1, 256, 16, 2000, 13, False, True),
+    # rows and KV heads enough for the tensor-core forms (rows of a CTA in front):
+    # one tile, several, one line of units
+    (256, "bf16", 2, 160, 64, 4, 64, 16, 48, 1, True, True),
+    (256, "bf16", 1, 300, 64, 8, 128, 32, 160, 2, False, True),
+    (256, "bf16", 2, 210, 48, 8, 128, 64, 704, 3, True, False),
+    (128, "f32", 2, 70, 64, 4, 64, 32, 96, 6, True, True),
+    (128, "f32", 1, 150, 64, 8, 128, 16, 272, 7, False, True),
+    (128, "f32", 1, 300, 48, 6, 256, 64, 192, 8, True, False),
+    (128, "f32", 1, 290, 14, 1, 128, 64, 4032, 9, True, True),
+    (128, "bf16", 1, 150, 64, 8, 256, 16, 144, 10, True, True),
+    (128, "bf16", 2, 300, 24, 4, 256, 128, 384, 11, False, True),
+    (128, "bf16", 1, 290, 14, 1, 256, 32, 2016, 12, False, False),
+    (128, "f32", 1, 290, 14, 1, 256, 16, 2000, 13, False, True),
+    (128, "bf16", 2, 100, 64, 4, 64, 16, 272, 14, True, True),
+    (128, "bf16", 4, 33, 64, 8, 128, 64, 704, 15, False, True),
+    (128, "bf16", 1, 290, 14, 1, 128, 32, 2016, 16, True, False),
 ]
 
 
-@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-B{c[1]}-Q{c[2]}-h{c[3]}of{c[4]}-d{c[5]}-blk{c[6]}-N{c[7]}" for c in WIDE])
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-{c[1]}-B{c[2]}-Q{c[3]}-h{c[4]}of{c[5]}-d{c[6]}-blk{c[7]}-N{c[8]}" for c in WIDE])
 def test_attend_tensor_core_forms(case):
-    act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc = case
+    rows, act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc = case
     p = bd.kv8_params(n_q, n_kv, d, block, N, act)
-    assert rows_of_a_cta(p, B, Q) == (256 if act == "bf16" and d <= 128 else 128)
+    assert rows_of_a_cta(p, B, Q) == rows
     check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 40 + seed, 0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_two_streams_on_one_line(d):
+    """A prompt chunk whose row tiles several CTAs share; every 32nd query checked."""
+    B, Q, n_q, n_kv, block, N = 1, 480, 14, 1, 32, 16384
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "bf16")
+    assert rows_of_a_cta(p, B, Q) == 256
+    n_vis = list(range(N - Q + 1, N + 1))
+    n_vis[64] = 0
+    clean, codes, exps, q, vis, z, _ = attend_inputs(("bf16", B, Q, n_q, n_kv, d, block, N, n_vis, True, False), 51)
+    out = torch.full((Q, n_q, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((bd.kv8_attend_workspace_bytes(p, B, Q, False),), 255, dtype=torch.uint8, device=DEV)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, sink=z.to(DEV), workspace=ws)
+    some = slice(0, Q, 32)
+    K, V = (kv8.values(clean[i].numpy(), exps[i].numpy(), block) for i in range(2))
+    ref, _, mag, load = kv8.attend(q[some].double().numpy(), n_vis[some], K, V, block, d ** -0.5, z.double().numpy())
+    within(np64(out[some]), ref, attend_tol("bf16", d, N, ref, mag, load, load.max()) + 1e-30, "out")
+    assert torch.isfinite(out).all()
 
 
 def test_attend_one_tile_of_rows_a_cta():
@@ -431,7 +453,7 @@ def test_attend_value_exponents_far_apart(act, Q, N, kind):
     own.  Logits do not depend on either, so neither may weights."""
     B, n_q, n_kv, d, block = 1, 4, 2, 64, 16
     p = bd.kv8_params(n_q, n_kv, d, block, N, act)
-    assert rows_of_a_cta(p, B, Q) == (16 if Q < 2000 else 256 if act == "bf16" else 128)
+    assert rows_of_a_cta(p, B, Q) == (16 if Q < 2000 else 128)
     g = torch.Generator().manual_seed(Q + N)
     codes = (torch.randn(2, B, n_kv, N, d, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     exps = torch.randint(115, 121, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8)
@@ -455,7 +477,7 @@ def test_attend_value_exponents_far_apart(act, Q, N, kind):
     # a term 2^7 2^(y - M) in fp16 is off by half its least step, 2^-25, at most where it is
     # subnormal: 2^-32 of the largest weight times 2^exponent, for each of N slots' codes up to 448
     # (few rows a KV head: 2^11 2^(y - M), so 2^-36)
-    top = N * 2.0 ** (-32 if Q == 2000 else -36) * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0) if kind == "far apart" else 0.0
+    top = N * 2.0 ** (-36 if Q < 2000 else -32) * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0) if kind == "far apart" else 0.0
     within(np64(out), ref, tol + top + 1e-36, "out")
     eps = (2 * d + 16) * U * rng + 8 * U * rng
     within(np64(acc), wref, (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * wref + 1e-30, "acc")
