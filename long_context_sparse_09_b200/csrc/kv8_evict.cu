@@ -9,6 +9,13 @@
 // moves what ends in slot block keep-1, whose own block may have to move
 // first.  kv8_move copies the others: sources lie at keep or above and
 // destinations below keep-1, so the copies are independent of one another.
+//
+// What bounds it: the bytes of the blocks that move, read and written once, and
+// for short caches the chain of votes and scans of kv8_select.  8 sequences of
+// 64K tokens cut to half (8 KV heads, d = 128, blocks of 64): 70 us for 361 MB, 79%
+// of the measured copy rate (256 threads a block and one load of each cache in
+// flight: 88 us; 64 threads 74, 8 loads 89).  One block over budget, 125 blocks a
+// head: 8.5 us in a graph, two kernels.
 #include "common.cuh"
 #include "kv8.h"
 
@@ -17,7 +24,7 @@ namespace csa {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 
 struct EvictArgs {
   const float* acc;
@@ -68,10 +75,21 @@ __device__ __forceinline__ void copy_block(const Kv8Cache& c, int64_t row, int N
   const uint4* vs = reinterpret_cast<const uint4*>(c.vc + (row * NB + src) * block_bytes);
   uint4* kd = reinterpret_cast<uint4*>(c.kc + (row * NB + dst) * block_bytes);
   uint4* vd = reinterpret_cast<uint4*>(c.vc + (row * NB + dst) * block_bytes);
-  for (int i = tid; i < n; i += threads) {
-    const uint4 a = ks[i], b = vs[i];
-    kd[i] = a;
-    vd[i] = b;
+  constexpr int U = 4;  // 16-byte loads of each cache in flight a thread (measured below)
+  for (int i0 = tid; i0 < n; i0 += U * threads) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * threads < n) {
+        a[u] = ks[i0 + u * threads];
+        b[u] = vs[i0 + u * threads];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * threads < n) {
+        kd[i0 + u * threads] = a[u];
+        vd[i0 + u * threads] = b[u];
+      }
   }
   if (tid == 0) {
     c.k_exp[row * NB + dst] = c.k_exp[row * NB + src];

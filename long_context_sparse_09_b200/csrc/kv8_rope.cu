@@ -159,9 +159,9 @@ qk_norm_rope_kernel(NormRopeArgs a, int R, int tokens, int q_ctas) {
     if (n == 0) break;
     T* dst = reinterpret_cast<T*>(a.out[w]) + r * a.out_stride[w] + (int64_t)first * a.d + lane * 8;
     if (w > w0) {
-      all_gains(w);
       src = reinterpret_cast<const T*>(a.x[1]) + r * a.stride[1] + (int64_t)first * a.d + lane * 8;
       fetch(first, n);
+      all_gains(w);
     }
     // factors of this lane's elements
     if constexpr (MODE == kInChunk) {
@@ -263,7 +263,9 @@ csa_status launch_group(const NormRopeArgs& a, int R, cudaStream_t st) {
   // four tokens a CTA where that still gives every SM work (a group's factors
   // then serve four times the heads); few tokens: one a CTA, and with fewer
   // tokens than SMs their heads spread over several
-  const int tokens = R >= 4 * sm_count() ? 4 : 1;
+  int tokens = R >= 4 * sm_count() ? 4 : 1;
+  // more of them where the heads leave groups idle and there are CTAs enough
+  while (tokens >= 4 && 2 * tokens <= per && per / (2 * tokens) >= a.heads[0] && R >= 8 * tokens * sm_count()) tokens *= 2;
   const bool spread = R < sm_count();
   const int q_ctas = spread ? (a.heads[0] + per - 1) / per : 0;
   const int gy = spread ? q_ctas + (a.heads[1] + per - 1) / per : 1;

@@ -338,6 +338,59 @@ def test_attend_extreme_values(Q):
         within(np64(out), ref, attend_tol("bf16", d, N, ref, mag, load, rng), f"q {qmag}")
 
 
+@pytest.mark.parametrize("act,Q,rows", [("bf16", 3, 16), ("f32", 3, 16), ("bf16", 400, 128), ("f32", 700, 128), ("bf16", 700, 256)])
+def test_attend_keeps_rows_apart(act, Q, rows):
+    """A query of NaN or infinities leaves the others' results as they are."""
+    B, n_q, n_kv, d, block, N = 1, 32, 4, 64, 16, 160
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    assert rows_of_a_cta(p, B, Q) == rows
+    case = (act, B, Q, n_q, n_kv, d, block, N, [N - 7] * Q, False, False)
+    _, codes, exps, q, vis, _, _ = attend_inputs(case, 61)
+    dc, de, qd, vd = codes.to(DEV), exps.to(DEV), q.to(DEV), vis.to(DEV)
+    want = torch.empty_like(qd)
+    bd.csa_kv8_attend(p, qd, vd, dc[0], de[0], dc[1], de[1], want)
+    for bad in (float("nan"), float("inf")):
+        got, qb = torch.empty_like(qd), qd.clone()
+        qb[1, 5, 3] = bad
+        bd.csa_kv8_attend(p, qb, vd, dc[0], de[0], dc[1], de[1], got)
+        assert got[1, 5].isnan().all()
+        got[1, 5] = want[1, 5]
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("act,Q,d", [("bf16", 1, 128), ("bf16", 2300, 64), ("f32", 700, 128), ("bf16", 700, 256)])
+def test_attend_in_two_graphs_and_on_two_streams(act, Q, d):
+    """Two captured calls with a workspace each, replayed on streams of their own
+    at the same time, with other lengths than at capture."""
+    B, n_q, n_kv, block, N = 1, 32, 4, 32, 352
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    runs = []
+    for seed in (71, 72):
+        case = (act, B, Q, n_q, n_kv, d, block, N, [N] * Q, False, True)
+        _, codes, exps, q, vis, _, w = attend_inputs(case, seed)
+        t = [x.to(DEV) for x in (codes, exps, q, vis, w)]
+        t.append(torch.empty_like(t[2]))
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s):
+            bd.csa_kv8_attend(p, t[2], t[3], t[0][0], t[1][0], t[0][1], t[1][1], t[5], acc=t[4])
+        runs.append((t, w.to(DEV), s, g))
+    for t, w, s, g in runs:
+        t[3].copy_(torch.arange(N - Q + 1, N + 1, dtype=torch.int32) if Q <= N else
+                   torch.arange(Q, dtype=torch.int32) % (N + 1))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for t, w, s, g in runs:
+            with torch.cuda.stream(s):
+                t[4].copy_(w)
+                g.replay()
+    torch.cuda.synchronize()
+    for t, w, s, g in runs:
+        out, acc = torch.empty_like(t[5]), w.clone()
+        bd.csa_kv8_attend(p, t[2], t[3], t[0][0], t[1][0], t[0][1], t[1][1], out, acc=acc)
+        assert torch.equal(out, t[5]) and torch.equal(acc, t[4])
+
+
 def test_attend_clamps_and_reports_a_length_beyond_the_cache():
     case = ("bf16", 2, 1, 4, 2, 64, 16, 64, [70, 64], False, False)
     _, codes, exps, q, _, _, _ = attend_inputs(case, 1, garbage=False)
