@@ -5,6 +5,11 @@
 // with max|x| <= 448 2^e (not below the one that the block's earlier slots
 // already have) and stores code = E4M3(x 2^-e).  If e grew, the earlier codes
 // are rescaled by a power of two, in place.
+//
+// What bounds it: for prompts the bytes; 32K tokens of 8 KV heads (d = 128, bf16)
+// 37.9 us for 201 MB, 81% of the measured copy rate (K and V of all heads of a
+// block of slots side by side in the grid: they lie together in the input).  For
+// single tokens one chain of loads and a vote: 32 sequences 2.6 us in a graph.
 #include "common.cuh"
 #include "kv8.h"
 

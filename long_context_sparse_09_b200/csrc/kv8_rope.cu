@@ -3,10 +3,16 @@
 //
 //   y = x * gain / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, a sin + b cos)
 //
-// A CTA owns one token: it forms the token's cos / sin once (fp64 turns,
-// reduced to a fraction of a turn before fp32) and walks the token's heads,
-// a group of lanes per head, 8 elements a lane and chunk.  The normalised row
-// goes through shared memory, so a pair's partner may sit anywhere in it.
+// A CTA owns a few tokens: it forms their cos / sin once (fp64 turns, reduced to
+// a fraction of a turn before fp32) and walks their heads, a group of lanes a
+// head, 8 elements a lane and chunk.  Where a pair's elements are in one lane's
+// chunk, or in the same place of two lanes' chunks, they meet in registers;
+// elsewhere the row goes through shared memory.
+//
+// What bounds it: for prompts the bytes, each read and written once; 32K tokens
+// of 64 + 8 heads (d = 128, bf16, 64 rotated dims) 222 us for 1.21 GB, 83% of the
+// measured copy rate.  For few tokens the chain position -> angles -> heads: four
+// tokens of 64 + 8 heads 3.0 us in a graph.
 #include "common.cuh"
 #include "kv8.h"
 

@@ -14,7 +14,8 @@ bf16, 2^-12 of fp16 (the type the attention's probabilities are rounded to).
   may truncate: a full step 2 U each), with q held to 2^-22 at least; a logit
   is off by at most eps = (2 d + 16) U * load + 8 U * |logit range| where
   load = max scale sum |q||k|, so weights by 2 eps; p is rounded to fp16
-  (2^-11 with the block's power of two, bf16 activations) or to two fp16
+  (2^-11 with the block's power of two, bf16 activations; in the tensor-core
+  forms after a polynomial that is off by 2^-18.5) or to two fp16
   terms (2^-22, fp32 activations) and summed over n / 16 steps of truncating
   fp32.  The output is off by at most (2 eps + p rounding + (n / 8 + 16) U)
   times sum p |v|, then its own rounding.
@@ -233,7 +234,7 @@ ATTEND = [
 
 def attend_tol(act, d, n, ref, mag, load, scale_range):
     eps = (2 * d + 16) * U * load[..., None] + 8 * U * scale_range
-    p_round = 2.0 ** -11 if act == "bf16" else 2.0 ** -22
+    p_round = 2.0 ** -11 + 2.0 ** -18 if act == "bf16" else 2.0 ** -22
     return HALF[act] * np.abs(ref) + (2 * eps + p_round + (n / 8 + 16) * U) * mag
 
 
