@@ -479,7 +479,7 @@ csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, 
  *           old value is not read); blocks no query of the sequence sees are
  *           left as they are
  *   workspace / ws_bytes         >= csa_kv8_attend_workspace_bytes(with_acc =
- *           acc != NULL).  Calls that may run at the same time need their
+ *           acc != NULL); 0 for calls that need none (then NULL will do).  Calls that may run at the same time need their
  *           own; nothing in it has to be kept between calls.
  * Results do not depend on timing: a repeated call gives the same bits. */
 size_t csa_kv8_attend_workspace_bytes(const csa_kv8_params* p, int B, int Q, int with_acc);

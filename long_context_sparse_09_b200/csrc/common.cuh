@@ -19,7 +19,7 @@ enum KernelKind {
   KK_PACK = 0, KK_GEMM, KK_FOLD, KK_WINDOW, KK_SCORES, KK_TOPK, KK_ATTN,
   KK_COMBINE, KK_PLAN, KK_TOPK_HIST, KK_TOPK_SELECT, KK_TOPK_FINAL, KK_DIAG,
   KK_ROPE_FREQS, KK_NORM_ROPE, KK_KV8_APPEND, KK_KV8_ATTEND, KK_KV8_COMBINE, KK_KV8_ACC,
-  KK_KV8_SELECT, KK_KV8_MOVE, KK_COUNT
+  KK_KV8_SELECT, KK_KV8_MOVE, KK_KV8_ATTEND_TC, KK_KV8_ATTEND_TC1, KK_COUNT
 };
 // Bracket one launch: begin() before it, end() after it, same stream.
 int prof_begin(int kind, cudaStream_t st);

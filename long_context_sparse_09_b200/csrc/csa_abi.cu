@@ -62,7 +62,7 @@ static const char* kKindNames[KK_COUNT] = {
     "pack_weights", "compress_gemm", "compress_fold", "compress_window", "index_scores",
     "topk_radix", "attend", "attend_combine", "index_plan", "topk_hist", "topk_select",
     "topk_final", "diag_bounded_wait", "rope_freqs", "qk_norm_rope", "kv8_append", "kv8_attend",
-    "kv8_combine", "kv8_acc", "kv8_select", "kv8_move"};
+    "kv8_combine", "kv8_acc", "kv8_select", "kv8_move", "kv8_attend_tc", "kv8_attend_tc1"};
 
 unsigned int* device_error_word() {
   // cudaGetSymbolAddress is per device; cache one address per device index.

@@ -637,6 +637,10 @@ struct Ws {
   size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
 
+int mma_unit(const csa_kv8_params& p) {  // slots of a unit here
+  return p.d == 64 ? Cfg<64, 1>::unit : p.d == 128 ? Cfg<128, 1>::unit : Cfg<256, 1>::unit;
+}
+
 // Which form the call takes: the one whose longest CTA is done first, at the time
 // that a unit takes (measured on long prompts, tenths of a us; the tensor-core
 // forms take 5 us more to set up).  64 heads, 8 of
@@ -646,14 +650,12 @@ struct Ws {
 // 2,580.
 enum Form { kMma, kTc, kTc1 };
 Form form_of(const csa_kv8_params& p, int B, int Q) {
-  constexpr int sms = 148;
   const bool f32 = p.act == CSA_F32;
   const long long rows = (long long)Q * (p.n_q / p.n_kv), heads = (long long)B * p.n_kv;
   auto cost = [&](int tile_rows, int unit, int join, int each) {
-    return each * line_units((rows + tile_rows - 1) / tile_rows * heads, p.N, unit, sms, join);
+    return each * line_units((rows + tile_rows - 1) / tile_rows * heads, p.N, unit, kSms, join);
   };
-  const int unit = p.d == 64 ? Cfg<64, 1>::unit : p.d == 128 ? Cfg<128, 1>::unit : Cfg<256, 1>::unit;
-  long long best = cost(kRows, unit, kJoinUnits, f32 ? 31 : 24);
+  long long best = cost(kRows, mma_unit(p), kJoinUnits, f32 ? 31 : 24);
   Form form = kMma;
   if (rows <= 2 * kRows) return form;
   if (!f32 && p.d <= 128) {
@@ -665,18 +667,32 @@ Form form_of(const csa_kv8_params& p, int B, int Q) {
   return c < best ? kTc1 : form;
 }
 
-// rows a CTA's piece holds
-int piece_rows(Form f) { return f == kTc ? kv8_attend_tc_rows() : f == kTc1 ? kv8_attend_tc1_rows() : kRows; }
+struct Way {
+  Form form;
+  int rows;         // query rows of a CTA
+  long long tiles;  // (sequence, row tile) pairs
+  bool planned;     // the units of all items on one line
+};
+Way way_of(const csa_kv8_params& p, int B, int Q) {
+  Way w;
+  w.form = form_of(p, B, Q);
+  w.rows = w.form == kTc ? kv8_attend_tc_rows() : w.form == kTc1 ? kv8_attend_tc1_rows() : kRows;
+  w.tiles = ((long long)Q * (p.n_q / p.n_kv) + w.rows - 1) / w.rows * B;
+  const int unit = w.form == kMma ? mma_unit(p) : w.form == kTc1 && p.d == 256 ? 64 : 128;
+  w.planned = w.tiles <= kMaxPlan && on_a_line(w.tiles * p.n_kv, p.N, unit, kSms, w.form == kMma ? kJoinUnits : kTcJoinUnits);
+  return w;
+}
 
 int acc_parts(const csa_kv8_params& p, int Q) {
   return (int)(((long long)Q * (p.n_q / p.n_kv) + kAccRows - 1) / kAccRows);
 }
 
 Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
-  const size_t rows = (size_t)B * Q * p.n_q, pieces = (size_t)kMaxGrid * 2 * piece_rows(form_of(p, B, Q));
+  const Way way = way_of(p, B, Q);
+  const size_t rows = (size_t)B * Q * p.n_q, pieces = way.planned ? (size_t)kMaxGrid * 2 * way.rows : 0;
   Ws w;
   w.plan = 0;
-  w.part_ml = w.plan + align_up((kMaxPlan + 1) * 4, 256);
+  w.part_ml = w.plan + (way.planned ? align_up((kMaxPlan + 1) * 4, 256) : 0);
   w.part_o = w.part_ml + pieces * 16;
   w.row_log = w.part_o + pieces * p.d * 4;
   w.acc_part = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
@@ -699,12 +715,10 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
-  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, C::unit, sms, kJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + C::unit - 1) / C::unit);
-    grid = sms;
+    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = units;
   }
   if (grid > 0x7fffffffll || items * kRows > 0x7fffffffll) return CSA_ERR_SHAPE;
@@ -736,12 +750,11 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   a.NSB = p.N / a.sub;
   a.shift = 31 - __builtin_clz((unsigned)p.block);
   a.sub_shift = 31 - __builtin_clz((unsigned)a.sub);
-  const Form form = form_of(p, B, Q);
-  const int rows = piece_rows(form);
-  const long long rts = ((long long)Q * a.G + rows - 1) / rows;
-  if (rts * B > 0x7fffffffll) return CSA_ERR_SHAPE;
-  a.RT = (int)rts;
-  a.E = (int)(rts * B);
+  const Way way = way_of(p, B, Q);
+  if (way.tiles > 0x7fffffffll) return CSA_ERR_SHAPE;
+  a.E = (int)way.tiles;
+  a.RT = a.E / B;
+  a.planned = way.planned;
   const bool few = (long long)Q * a.G <= kAccFew;
   const int tiles = (a.NSB + (few ? kAccThreads : 32) - 1) / (few ? kAccThreads : 32), parts = acc_parts(p, Q);
   const long long blocks = (long long)B * a.H * a.NB;
@@ -763,9 +776,9 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
     a.blk_log = (float*)(base + w.blk_log);
   }
   csa_status r;
-  if (form == kTc)
+  if (way.form == kTc)
     r = launch_kv8_attend_tc(p, a, st);
-  else if (form == kTc1)
+  else if (way.form == kTc1)
     r = launch_kv8_attend_tc1(p, a, st);
   else if (!tma_available())
     return CSA_ERR_CUDA;

@@ -17,6 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Tensor-core forms: 524 queries (7 heads a KV head, 2 of them, d = 128, bf16) over
 // 1024 slots: one line 45 us, a CTA an item (8 units) 35; over 2048: 47.4 and 53.6.
 constexpr int kTcJoinUnits = 8;
+constexpr int kSms = 148;          // SMs that the choices below count with
 constexpr int kMaxPlan = 1024;     // (sequence, row tile) pairs that the line of units holds
 constexpr int kMaxGrid = 160;      // CTAs whose pieces the workspace holds (148 SMs)
 // Value exponents within +-kTame: sums relative to the maximum of y neither

@@ -456,19 +456,17 @@ csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
   const int smem = Tc<D>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
-  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, kTcTile, sms, kTcJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + kTcTile - 1) / kTcTile);
-    grid = sms;
+    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = units;
   }
   if (items * (kTcRows / kTcJoinRows) > 0x7fffffffll || (long long)a.Q * a.G + kTcRows > 0x7fffffffll ||
       (long long)a.B * a.H > 0x7fffffffll)
     return CSA_ERR_SHAPE;
   csa_status ok = CSA_OK;
-  CSA_LAUNCH(KK_KV8_ATTEND, st,
+  CSA_LAUNCH(KK_KV8_ATTEND_TC, st,
              if (launch_maybe_pdl(true, kern, dim3((unsigned)grid), dim3(kTcThreads), smem, st, a) !=
                  cudaSuccess) ok = CSA_ERR_CUDA);
   if (a.planned)

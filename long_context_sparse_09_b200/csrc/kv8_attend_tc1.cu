@@ -516,19 +516,17 @@ csa_status launch_tc1(AttnArgs& a, cudaStream_t st) {
   const int smem = Tc1<T, D>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
-  const int sms = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-  a.planned = a.E <= kMaxPlan && on_a_line(items, a.N, Tc1<T, D>::KT, sms, kTcJoinUnits);
   long long grid = items;
   if (a.planned) {
     const long long units = items * ((a.N + Tc1<T, D>::KT - 1) / Tc1<T, D>::KT);
-    grid = sms;
+    grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = units;
   }
   if (items * (kTc1Rows / kTcJoinRows) > 0x7fffffffll || (long long)a.Q * a.G + kTc1Rows > 0x7fffffffll ||
       (long long)a.B * a.H > 0x7fffffffll)
     return CSA_ERR_SHAPE;
   csa_status ok = CSA_OK;
-  CSA_LAUNCH(KK_KV8_ATTEND, st,
+  CSA_LAUNCH(KK_KV8_ATTEND_TC1, st,
              if (launch_maybe_pdl(true, kern, dim3((unsigned)grid), dim3(kTcThreads), smem, st, a) !=
                  cudaSuccess) ok = CSA_ERR_CUDA);
   if (a.planned)

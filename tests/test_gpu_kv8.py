@@ -21,6 +21,8 @@ bf16, 2^-12 of fp16 (the type the attention's probabilities are rounded to).
   times sum p |v|, then its own rounding.
 * append and eviction: exact.
 """
+import contextlib
+
 import numpy as np
 import pytest
 import torch
@@ -344,12 +346,12 @@ def test_attend_keeps_rows_apart(act, Q, rows):
     """A query of NaN or infinities leaves the others' results as they are."""
     B, n_q, n_kv, d, block, N = 1, 32, 4, 64, 16, 160
     p = bd.kv8_params(n_q, n_kv, d, block, N, act)
-    assert rows_of_a_cta(p, B, Q) == rows
     case = (act, B, Q, n_q, n_kv, d, block, N, [N - 7] * Q, False, False)
     _, codes, exps, q, vis, _, _ = attend_inputs(case, 61)
     dc, de, qd, vd = codes.to(DEV), exps.to(DEV), q.to(DEV), vis.to(DEV)
     want = torch.empty_like(qd)
-    bd.csa_kv8_attend(p, qd, vd, dc[0], de[0], dc[1], de[1], want)
+    with rows_of_a_cta(rows):
+        bd.csa_kv8_attend(p, qd, vd, dc[0], de[0], dc[1], de[1], want)
     for bad in (float("nan"), float("inf")):
         got, qb = torch.empty_like(qd), qd.clone()
         qb[1, 5, 3] = bad
@@ -435,12 +437,18 @@ def test_attend_many_rows(case):
     check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 20 + seed, 0.5)
 
 
-def rows_of_a_cta(p, B, Q):
-    """Query rows that a CTA of the call owns, from the size of its pieces:
-    16 (mma.sync), 256 or 128 (tcgen05)."""
-    small = bd.kv8_params(p.n_kv, p.n_kv, p.d, p.block, p.block, "bf16")   # one row: 16
-    a, b = bd.kv8_attend_workspace_bytes(p, B, Q, False), bd.kv8_attend_workspace_bytes(small, 1, 1, False)
-    return 16 + (a - b) // (2 * 160 * (16 + 4 * p.d))
+@contextlib.contextmanager
+def rows_of_a_cta(rows):
+    """The attention calls inside go to the form whose CTAs own that many query
+    rows (256 and 128: tcgen05)."""
+    bd.profile_enable(True)
+    try:
+        bd.profile_collect()
+        yield
+        ran = {k for k, (_, n) in bd.profile_collect().items() if n and k.startswith("kv8_attend")}
+    finally:
+        bd.profile_enable(False)
+    assert ran == {{16: "kv8_attend", 256: "kv8_attend_tc", 128: "kv8_attend_tc1"}[rows]}
 
 
 WIDE = [
@@ -466,9 +474,8 @@ WIDE = [
 @pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-{c[1]}-B{c[2]}-Q{c[3]}-h{c[4]}of{c[5]}-d{c[6]}-blk{c[7]}-N{c[8]}" for c in WIDE])
 def test_attend_tensor_core_forms(case):
     rows, act, B, Q, n_q, n_kv, d, block, N, seed, sink, acc = case
-    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
-    assert rows_of_a_cta(p, B, Q) == rows
-    check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 40 + seed, 0.5)
+    with rows_of_a_cta(rows):
+        check_attend((act, B, Q, n_q, n_kv, d, block, N, spread_vis(B, Q, N, seed), sink, acc), 40 + seed, 0.5)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -476,14 +483,14 @@ def test_attend_two_streams_on_one_line(d):
     """A prompt chunk whose row tiles several CTAs share; every 32nd query checked."""
     B, Q, n_q, n_kv, block, N = 1, 480, 14, 1, 32, 16384
     p = bd.kv8_params(n_q, n_kv, d, block, N, "bf16")
-    assert rows_of_a_cta(p, B, Q) == 256
     n_vis = list(range(N - Q + 1, N + 1))
     n_vis[64] = 0
     clean, codes, exps, q, vis, z, _ = attend_inputs(("bf16", B, Q, n_q, n_kv, d, block, N, n_vis, True, False), 51)
     out = torch.full((Q, n_q, d), float("nan"), dtype=torch.bfloat16, device=DEV)
     ws = torch.full((bd.kv8_attend_workspace_bytes(p, B, Q, False),), 255, dtype=torch.uint8, device=DEV)
     dc, de = codes.to(DEV), exps.to(DEV)
-    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, sink=z.to(DEV), workspace=ws)
+    with rows_of_a_cta(256):
+        bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, sink=z.to(DEV), workspace=ws)
     some = slice(0, Q, 32)
     K, V = (kv8.values(clean[i].numpy(), exps[i].numpy(), block) for i in range(2))
     ref, _, mag, load = kv8.attend(q[some].double().numpy(), n_vis[some], K, V, block, d ** -0.5, z.double().numpy())
@@ -507,7 +514,6 @@ def test_attend_value_exponents_far_apart(act, Q, N, kind):
     own.  Logits do not depend on either, so neither may weights."""
     B, n_q, n_kv, d, block = 1, 4, 2, 64, 16
     p = bd.kv8_params(n_q, n_kv, d, block, N, act)
-    assert rows_of_a_cta(p, B, Q) == (16 if Q < 2000 else 128)
     g = torch.Generator().manual_seed(Q + N)
     codes = (torch.randn(2, B, n_kv, N, d, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     exps = torch.randint(115, 121, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8)
@@ -523,7 +529,8 @@ def test_attend_value_exponents_far_apart(act, Q, N, kind):
     acc = torch.zeros(B, n_kv, NB, device=DEV)
     out = torch.empty(B * Q, n_q, d, dtype=DT[act], device=DEV)
     dc, de = codes.to(DEV), exps.to(DEV)
-    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, acc=acc)
+    with rows_of_a_cta(16 if Q < 2000 else 128):
+        bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, acc=acc)
     K, V = (kv8.values(codes[i].numpy(), exps[i].numpy(), block) for i in range(2))
     ref, wref, mag, load = kv8.attend(q.double().numpy(), vis.tolist(), K, V, block, d ** -0.5)
     rng = load.max()
