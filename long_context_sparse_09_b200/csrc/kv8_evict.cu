@@ -14,8 +14,9 @@
 // for short caches the chain of votes and scans of kv8_select.  8 sequences of
 // 64K tokens cut to half (8 KV heads, d = 128, blocks of 64): 70 us for 361 MB, 79%
 // of the measured copy rate (256 threads a block and one load of each cache in
-// flight: 88 us; 64 threads 74, 8 loads 89).  One block over budget, 125 blocks a
-// head: 8.5 us in a graph, two kernels.
+// flight: 88 us; 64 threads 74, 8 loads 89).  A cache with few blocks
+// beyond the budget is done in one kernel: 4 sequences, 125 blocks a head, one of
+// them to go, 10.6 us as a graph of one call (12.7 with kv8_move behind it).
 #include "common.cuh"
 #include "kv8.h"
 
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kMoveThreads = 128;
+constexpr int kFewMoves = 8;  // so many blocks a head are moved by kv8_select itself
 
 struct EvictArgs {
   const float* acc;
@@ -35,6 +37,7 @@ struct EvictArgs {
   int32_t* n_tok_out;
   unsigned* err;
   int H, N, NB, block, d, keep, recent;
+  int alone;  // no kv8_move: at most kFewMoves blocks go, and n_tok_out is not n_tok
 };
 
 // NaN counts as the least weight
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
   __shared__ unsigned sh[33];
   __shared__ unsigned hist[256];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_need, s_moves, moves[kFewMoves];
   pdl_wait();
   const int64_t row = blockIdx.x;
   const int b = (int)(row / a.H), tid = threadIdx.x, lane = tid & 31;
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
   float* acc_out = a.acc_out + row * a.NB;
   int32_t* kept = a.kept + row * a.keep;
   const int nb = bad ? 0 : (int)(((long long)n + a.block - 1) / a.block);
+  if (a.alone && row % a.H == 0 && tid == 0) a.n_tok_out[b] = nb > a.keep ? n - (nb - a.keep) * a.block : n;
   if (nb <= a.keep) {  // nothing goes
     for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = i < nb ? i : -1;
     for (int i = tid; i < a.NB; i += kSelThreads) {
@@ -195,6 +199,8 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
   }
   __syncthreads();
   count_words(stay, before, words, sh);
+  if (tid == 0) s_moves = 0;
+  __syncthreads();
   // what each slot block holds
   const int last = a.keep - 1;
   const int fixed = rank_of(stay, before, last);  // kept blocks that stay where they are
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
     }
     kept[i] = src;
     if (i < last) acc_out[i] = acc[src];
+    if (a.alone && i < last && src >= a.keep) moves[atomicAdd(&s_moves, 1)] = i;  // (their order does not matter)
   }
   // block keep-1, where it stays, goes to the first free slot block; then the
   // last block takes its place (the same thread moves the same bytes)
@@ -225,6 +232,9 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(EvictArgs a) {
   __syncthreads();  // acc_out may be acc: all of it has been read
   if (tid == 0) acc_out[last] = acc_last;
   for (int i = a.keep + tid; i < a.NB; i += kSelThreads) acc_out[i] = 0.f;
+  if (a.alone)  // (after the barrier: kept and the list are complete)
+    for (int m = tid / kMoveThreads; m < s_moves; m += kSelThreads / kMoveThreads)
+      copy_block(a.c, row, a.NB, block_bytes, kept[moves[m]], moves[m], tid % kMoveThreads, kMoveThreads);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(EvictArgs a) {
@@ -255,6 +265,9 @@ csa_status launch_kv8_evict(const csa_kv8_params& p, int B, int keep, int recent
   if (a.err == nullptr) return CSA_ERR_CUDA;
   a.H = p.n_kv; a.N = p.N; a.NB = p.N / p.block; a.block = p.block; a.d = p.d;
   a.keep = keep; a.recent = recent;
+  // a cache with a few blocks beyond the budget, as a decode loop keeps it: one
+  // kernel (n_tok_out has to be other memory: all heads of a sequence read n_tok)
+  a.alone = a.NB - keep <= kFewMoves && (n_tok_out + B <= n_tok || n_tok + B <= n_tok_out);
   const int smem = (a.NB + 31) / 32 * 8;
   if (smem > 40 * 1024 && !set_kernel_smem((const void*)kv8_select_kernel, smem)) return CSA_ERR_CUDA;
   const long long rows = (long long)B * p.n_kv;
@@ -263,6 +276,7 @@ csa_status launch_kv8_evict(const csa_kv8_params& p, int B, int keep, int recent
   CSA_LAUNCH(KK_KV8_SELECT, st,
              if (launch_maybe_pdl(true, kv8_select_kernel, dim3((unsigned)rows), dim3(kSelThreads), smem, st,
                                   a) != cudaSuccess) ok = CSA_ERR_CUDA);
+  if (a.alone) return ok != CSA_OK ? ok : last_launch_status();
   CSA_LAUNCH(KK_KV8_MOVE, st,
              if (launch_maybe_pdl(true, kv8_move_kernel, dim3((unsigned)(rows * keep)),
                                   dim3(kMoveThreads), 0, st, a) != cudaSuccess) ok = CSA_ERR_CUDA);

@@ -554,6 +554,9 @@ EVICT = [
     (1, 2, 256, 16, 1024, [1009], 63, 3),
     (2, 1, 64, 16, 40000, [39990, 20001], 700, 8),
     (1, 1, 64, 128, 8192, [8191], 64, 1),
+    (3, 2, 128, 32, 1056, [1056, 800, 801], 25, 2),
+    (2, 3, 64, 16, 640, [639, 512], 38, 30),
+    (1, 4, 128, 64, 4096, [4090], 64, 1),
 ]
 
 
