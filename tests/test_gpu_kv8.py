@@ -615,6 +615,47 @@ def test_evict_reports_a_bad_length():
     assert torch.equal(dc.cpu(), codes)
 
 
+# --------------------------------------------------------- offsets of 33 bits --
+@pytest.mark.parametrize("act,Q,rows", [("bf16", 1, 16), ("bf16", 64, 256), ("f32", 48, 128)])
+def test_a_cache_beyond_4_gb(act, Q, rows):
+    """Append, attention and eviction in the last sequence of a cache of 5.4 GB of
+    keys, the others empty."""
+    B, n_q, n_kv, d, block, N, T = 5, 64, 8, 128, 64, 1 << 20, 200
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    g = torch.Generator().manual_seed(81)
+    kc, vc = (torch.empty(B, n_kv, N, d, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ke, ve = (torch.empty(B, n_kv, N // block, dtype=torch.uint8, device=DEV) for _ in range(2))
+    x = torch.randn(2, B, T, n_kv, d, generator=g).to(DT[act])
+    n = torch.tensor([0] * (B - 1) + [T], dtype=torch.int32, device=DEV)
+    xd = x.to(DEV)
+    bd.csa_kv8_append(p, xd[0], xd[1], torch.zeros_like(n), kc, ke, vc, ve, n_new=n)
+    c, e = np.zeros((2, 1, n_kv, 256, d), np.uint8), np.zeros((2, 1, n_kv, 4), np.uint8)
+    for i, (codes, exps) in enumerate(((kc, ke), (vc, ve))):
+        kv8.append(x[i, B - 1:].double().numpy(), [0], [T], c[i], e[i], block)
+        assert np.array_equal(codes[B - 1, :, :T].cpu().numpy(), c[i, 0, :, :T])
+        assert np.array_equal(exps[B - 1, :, :4].cpu().numpy(), e[i, 0])
+    q = (torch.randn(B * Q, n_q, d, generator=g) * 2).to(DT[act])
+    vis = torch.cat([torch.zeros((B - 1) * Q, dtype=torch.int32), T - Q + 1 + torch.arange(Q, dtype=torch.int32)])
+    out = torch.full((B * Q, n_q, d), float("nan"), dtype=DT[act], device=DEV)
+    with rows_of_a_cta(rows):
+        bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), kc, ke, vc, ve, out)
+    assert (out[:(B - 1) * Q] == 0).all()
+    K, V = (kv8.values(c[i], e[i], block) for i in range(2))
+    ref, _, mag, load = kv8.attend(q[(B - 1) * Q:].double().numpy(), vis[(B - 1) * Q:].tolist(), K, V, block, d ** -0.5)
+    within(np64(out[(B - 1) * Q:]), ref, attend_tol(act, d, 256, ref, mag, load, load.max()) + 1e-30, "out")
+    if Q > 1:
+        return
+    acc = torch.rand(B, n_kv, N // block, generator=g).to(DEV)
+    want = kv8.evict(acc[B - 1:, :, :4].cpu().numpy(), [T], 2, 1, block)[0][0]
+    kept = torch.empty(B, n_kv, 2, dtype=torch.int32, device=DEV)
+    bd.csa_kv8_evict(p, 2, 1, acc, n, kc, ke, vc, ve, kept, acc, n)
+    assert n.tolist() == [0] * (B - 1) + [T - 2 * block]
+    assert np.array_equal(kept[B - 1].cpu().numpy(), want)
+    for h in range(n_kv):
+        blocks = c[0, 0, h].reshape(4, block, d)[want[h]].reshape(-1, d)[:T - 2 * block]
+        assert np.array_equal(kc[B - 1, h, :T - 2 * block].cpu().numpy(), blocks)
+
+
 # ------------------------------------------------------------ run together --
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_a_decode_run_with_eviction(act):
