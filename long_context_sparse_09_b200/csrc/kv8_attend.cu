@@ -78,7 +78,10 @@ struct Cfg {
   static_assert(kRows * (D + 4) * 4 <= warp_ring && total + 1024 <= 232448, "shared memory");
 };
 
-template <typename T, int D, int SPLIT>
+// WEIGHTS: a CTA has the only row tile of a sequence and KV head to the end, and adds
+// its block weights up itself (a kernel of its own for it: the code would cost
+// the long walk 1%)
+template <typename T, int D, int SPLIT, bool WEIGHTS>
 __global__ void __launch_bounds__(Cfg<D, SPLIT>::threads, 1)
 kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                AttnArgs a) {
@@ -495,6 +498,24 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
       }
     }
+    if constexpr (WEIGHTS) {
+      __syncthreads();  // blk_log and row_log of the item's rows are this CTA's
+      const int per = a.block / a.sub;
+      for (int i = tid; i < a.NB; i += C::threads) {
+        float sum = 0.f;
+        bool seen = false;
+        for (int r = 0; r < a.Q * a.G; ++r) {
+          const int64_t lrow = head * a.Q * a.G + r;
+          for (int k = 0; k < per; ++k)
+            if ((i * per + k) * a.sub < rowinfo[r].x) {
+              sum += fast_exp2(a.blk_log[lrow * a.NSB + i * per + k] - a.row_log[lrow]);
+              seen = true;
+            }
+        }
+        float* acc = a.acc + head * a.NB + i;
+        if (seen) *acc = a.decay == 0.f ? sum : fmaf(a.decay, *acc, sum);
+      }
+    }
     ++segment;
     cur.local = local0 + count - 1;
     if (u < u1) cur.next(before, nmax, a.H, a.E);
@@ -703,7 +724,7 @@ Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
 }
 
 template <typename T, int D, int SPLIT>
-csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, cudaStream_t st) {
+csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, bool weights, cudaStream_t st) {
   using C = Cfg<D, SPLIT>;
   CUtensorMap tmK, tmV;
   const uint64_t slots = (uint64_t)a.B * a.H * a.N;
@@ -711,7 +732,7 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, c
   const uint32_t box = D == 64 ? kTile / 2 : kTile;
   if (!make_tmap_bf16(&tmK, c.kc, rows, cols, box) || !make_tmap_bf16(&tmV, c.vc, rows, cols, box))
     return CSA_ERR_CUDA;
-  auto kern = kv8_attend_mma<T, D, SPLIT>;
+  auto kern = weights ? kv8_attend_mma<T, D, SPLIT, true> : kv8_attend_mma<T, D, SPLIT, false>;
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
@@ -775,6 +796,7 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
     a.row_log = (float*)(base + w.row_log);
     a.blk_log = (float*)(base + w.blk_log);
   }
+  const bool weights = acc != nullptr && way.form == kMma && !way.planned && a.RT == 1;
   csa_status r;
   if (way.form == kTc)
     r = launch_kv8_attend_tc(p, a, st);
@@ -783,13 +805,13 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
   else if (!tma_available())
     return CSA_ERR_CUDA;
   else if (p.act == CSA_F32)
-    r = p.d == 64 ? launch_mma<float, 64, 2>(p, c, a, st)
-        : p.d == 128 ? launch_mma<float, 128, 2>(p, c, a, st) : launch_mma<float, 256, 2>(p, c, a, st);
+    r = p.d == 64 ? launch_mma<float, 64, 2>(p, c, a, weights, st)
+        : p.d == 128 ? launch_mma<float, 128, 2>(p, c, a, weights, st) : launch_mma<float, 256, 2>(p, c, a, weights, st);
   else
-    r = p.d == 64 ? launch_mma<__nv_bfloat16, 64, 1>(p, c, a, st)
-        : p.d == 128 ? launch_mma<__nv_bfloat16, 128, 1>(p, c, a, st)
-                     : launch_mma<__nv_bfloat16, 256, 1>(p, c, a, st);
-  if (r != CSA_OK || !acc) return r;
+    r = p.d == 64 ? launch_mma<__nv_bfloat16, 64, 1>(p, c, a, weights, st)
+        : p.d == 128 ? launch_mma<__nv_bfloat16, 128, 1>(p, c, a, weights, st)
+                     : launch_mma<__nv_bfloat16, 256, 1>(p, c, a, weights, st);
+  if (r != CSA_OK || !acc || weights) return r;
   float* part = (float*)(base + w.acc_part);
   csa_status ok = CSA_OK;
   CSA_LAUNCH(KK_KV8_ACC, st,
