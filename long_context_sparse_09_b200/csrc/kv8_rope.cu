@@ -10,7 +10,7 @@
 // elsewhere the row goes through shared memory.
 //
 // What bounds it: for prompts the bytes, each read and written once; 32K tokens
-// of 64 + 8 heads (d = 128, bf16, 64 rotated dims) 222 us for 1.21 GB, 83% of the
+// of 64 + 8 heads (d = 128, bf16, 64 rotated dims) 208 us for 1.21 GB, 88% of the
 // measured copy rate.  For few tokens the chain position -> angles -> heads: four
 // tokens of 64 + 8 heads 3.0 us in a graph.
 #include "common.cuh"
@@ -266,10 +266,11 @@ qk_norm_rope_kernel(NormRopeArgs a, int R, int tokens, int q_ctas) {
 template <typename T, int MODE, int NC, int G>
 csa_status launch_group(const NormRopeArgs& a, int R, cudaStream_t st) {
   constexpr int per = kNrThreads / G;
-  // four tokens a CTA where that still gives every SM work (a group's factors
-  // then serve four times the heads); few tokens: one a CTA, and with fewer
-  // tokens than SMs their heads spread over several
-  int tokens = R >= 4 * sm_count() ? 4 : 1;
+  // four or eight tokens a CTA where that still gives every SM work (a group's
+  // factors then serve so many more heads; 32K tokens of 64 + 8 heads: 222 and 208
+  // us, 1,500 of 32 + 8: 12.7 and 14.7); few tokens: one a CTA, and with fewer tokens
+  // than SMs their heads spread over several
+  int tokens = R >= 16 * sm_count() ? 8 : R >= 4 * sm_count() ? 4 : 1;
   // more of them where the heads leave groups idle and there are CTAs enough
   while (tokens >= 4 && 2 * tokens <= per && per / (2 * tokens) >= a.heads[0] && R >= 8 * tokens * sm_count()) tokens *= 2;
   const bool spread = R < sm_count();

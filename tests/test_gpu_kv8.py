@@ -69,6 +69,14 @@ NORM = [
     ("f32", 2, 17, 4, 40, 2, 38, "half", "none", False, False),
     ("bf16", 4, 3, 2, 128, 0, 0, "half", "none", True, True),
     ("bf16", 5, 2, 1, 264, 264, 0, "interleaved", "linear", True, True),
+    # several tokens a CTA: 4, 8, and more where heads are few
+    ("f32", 701, 5, 2, 128, 128, 0, "interleaved", "parts", True, True),
+    ("bf16", 2501, 33, 2, 64, 32, 32, "half", "linear", True, True),
+    ("bf16", 19001, 1, 1, 64, 64, 0, "half", "none", True, True),
+    ("bf16", 9603, 4, 3, 96, 48, 8, "interleaved", "none", True, True),
+    ("bf16", 2603, 2, 1, 256, 34, 5, "half", "none", True, False),
+    ("f32", 2402, 1, 1, 512, 64, 448, "interleaved", "none", True, True),
+    ("f32", 4801, 2, 0, 256, 256, 0, "half", "none", True, True),
 ]
 SCALE = dict(factor=8.0, orig_len=4096.0)
 
