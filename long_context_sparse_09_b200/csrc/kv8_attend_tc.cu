@@ -19,13 +19,16 @@
 // in one ring.  All tiles of the call lie on one line, cut evenly over the SMs;
 // the pieces of items that several CTAs share are joined by kv8_join.
 //
-// What bounds it: a stream's chain of softmax (3,000 cycles a tile), P V and
-// Q K^T (1,060), of which two run against each other; the tensor cores work 44%
-// of the time.  2048 queries of 64 heads over 32K slots of 8 KV heads (d = 128):
-// 2.15 ms, 990 TFLOP/s, 61% of the measured bf16 rate; on mma.sync
-// (kv8_attend.cu) 11.4 ms.  Tiles of 64 slots with two S buffers a stream took
-// 2.56 ms (a product with N = 64 costs as much as one with N = 128), the
-// products issued by the softmax warps themselves 2.6 ms.
+// What bounds it: forming P.  The two softmax warps of a scheduler take 2,015
+// cycles a tile for their exponentials, sums and packing alone (measured without
+// products; 1,536 of them the special function unit's), 470 for the maxima, next
+// to 2,060 of products for both streams; without P the kernel takes 1.37 ms, with
+// half of it 1.50.  2048 queries of 64 heads over 32K slots of 8 KV heads (d = 128):
+// 2.17 ms, 980 TFLOP/s, 61% of the measured bf16 rate (2.39 in long runs, under the
+// power limit); on mma.sync (kv8_attend.cu) 11.4 ms.  Tiles of 64 slots with two S
+// buffers a stream took 2.49 ms (a product with N = 64 costs as much as one with N =
+// 128), the products issued by the softmax warps themselves 2.6 ms, four softmax
+// warpgroups of half a tile each 2.94.
 #include "kv8_attend_tc.cuh"
 
 namespace csa {
@@ -43,8 +46,8 @@ struct Tc {
   static constexpr int NS = D == 64 ? 8 : 4;         // K and V tiles in the ring
   static constexpr int q = 0;
   static constexpr int ring = 2 * row_tile;
-  static constexpr int table = ring + NS * row_tile;           // [8 warps][2][8] float4
-  static constexpr int plan = table + 8 * 2 * 8 * 16;          // units before, n_max: [E + 1], [E]
+  static constexpr int table = ring + NS * row_tile;           // [8 warps][2][32] float4
+  static constexpr int plan = table + 8 * 2 * 32 * 16;         // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
   static constexpr int total = bars + (2 * NS + 8) * 8 + 16;
 };
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
     const int st = warp >> 2, row = tid & 127;         // stream, row in it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = lanes + st * 128, tO = lanes + 256 + st * D;
-    float4* table = reinterpret_cast<float4*>(sm + C::table) + warp * 16;
+    float4* table = reinterpret_cast<float4*>(sm + C::table) + warp * 64;
     // the scale's sign goes into the queries, its power of two into their
     // exponents, its mantissa into the keys' factors
     const float qsign = a.scale2 < 0.f ? -1.f : 1.f;
@@ -134,12 +137,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       if (count > 0) {
         // ---- Q: fp16 times a power of two per row, largest magnitude in [2^14, 2^15)
         const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + (live ? row_at() : 0));
-        uint4 raw[D / 8];
+        // (read twice: held in registers it would have the loop's values spilled)
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          raw[c] = live ? q[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          const uint4 v = live ? q[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t m0 = (w[i] << 16) & 0x7fff0000u, m1 = w[i] & 0x7fff0000u;
@@ -150,9 +153,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         const int qe = top ? max((int)(top >> 23) - 127 - 14, -126) : 0;
         qscale = pow2i(clamp_exp(qe + scale_e));
         const float f = pow2i(-qe) * qsign;
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          const uint4 v = live ? q[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -166,10 +170,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       }
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
-      // exponents of the tile's 16-slot groups: lanes 0-7 hold one of each
+      // exponents of the 16-slot groups of four tiles, a lane one of each; their
+      // factors go to a table four tiles at a time
       int ke = 127, ve = 127;
       auto fetch = [&](int i) {
-        const int s = (local0 + i) * kTcTile + (lane & 7) * 16;
+        const int s = (local0 + i) * kTcTile + lane * 16;
         ke = ve = 127;
         if (s < cur.n) {
           const int64_t at = (int64_t)head * a.NB + (s >> a.shift);
@@ -181,12 +186,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 #pragma unroll 1
       for (int i = 0; i < count; ++i, ++tiles) {
         const int s0 = (local0 + i) * kTcTile;
-        float4* tab = table + (tiles & 1) * 8;
-        const int vl = ve - 127;
-        if (lane < 8) tab[lane] = make_float4(scale_m * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
-        const bool turn = !wild && __any_sync(0xffffffffu, vl < -kTame || vl > kTame);
-        __syncwarp();
-        if (i + 1 < count) fetch(i + 1);
+        bool turn = false;
+        if ((i & 3) == 0) {
+          const int vl = ve - 127;
+          table[(i & 4) * 8 + lane] =
+              make_float4(scale_m * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
+          turn = !wild && __any_sync(0xffffffffu, vl < -kTame || vl > kTame);
+          __syncwarp();
+          if (i + 4 < count) fetch(i + 4);
+        }
+        const float4* tab = table + (i & 7) * 8;
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[st], tiles & 1, abort_sm))) { ok = false; break; }
         tc_fence_after();
         if (__any_sync(0xffffffffu, vis < s0 + kTcTile)) {  // masked slots: -inf, back into S
