@@ -684,7 +684,7 @@ Form form_of(const csa_kv8_params& p, int B, int Q) {
     if (c < best) best = c, form = kTc;
   }
   const long long c = 50 + cost(kv8_attend_tc1_rows(), p.d == 256 ? 64 : 128, kTcJoinUnits,
-                           p.d == 64 ? 19 : p.d == 128 ? (f32 ? 23 : 19) : (f32 ? 32 : 15));
+                           p.d == 64 ? (f32 ? 21 : 19) : p.d == 128 ? (f32 ? 26 : 19) : (f32 ? 34 : 15));
   return c < best ? kTc1 : form;
 }
 

@@ -15,9 +15,10 @@
 // What bounds it: the softmax of a tile (about 3,000 cycles of one warpgroup, two
 // of them running) against its products.  The last 2048 queries over 8K slots, 64
 // heads, 8 KV heads: bf16, d = 256 1.17 ms (820
-// TFLOP/s), fp32, d = 128 0.89 ms (540 TFLOP/s of fp32 attention, twice that in fp16
-// products), fp32, d = 64 0.72 ms; on mma.sync (kv8_attend.cu) 5.2, 3.25 and 2.25 ms.
-// fp32 at d = 256 has room for one K and one V tile only: 2.48 ms (mma.sync 6.7).
+// TFLOP/s), fp32, d = 128 1.02 ms (470 TFLOP/s of fp32 attention, twice that in fp16
+// products; 0.89 without the sums in parts), fp32, d = 64 0.78 ms; on mma.sync
+// (kv8_attend.cu) 5.2, 3.25 and 2.25 ms.  fp32 at d = 256 has room for one K and one
+// V tile only: 2.57 ms (mma.sync 6.7).
 #include "kv8_attend_tc.cuh"
 
 namespace csa {
@@ -33,6 +34,12 @@ struct Tc1 {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of q and p
   static constexpr int KT = D == 256 ? 64 : 128;        // slots of a tile
   static constexpr int NG = KT / 16;
+  // fp32: after so many tiles (2048 slots; even) O is added to the row's sum in
+  // memory and starts anew.  The tensor cores cut off what they add to an
+  // accumulator, always towards zero: over 16K slots O shrank by 1.4e-5 (relative
+  // error 1.7e-5; with the parts 4.4e-6, with parts of 1024 slots 3.1e-6, plain fp32
+  // torch 2.6e-6).  It costs 14% (d = 128; parts of 1024: 24%).
+  static constexpr int flush = SPLIT == 2 ? 2048 / KT : 0;
   static constexpr int q_term = kTc1Rows * D * 2;       // a term of the queries
   static constexpr int kv_tile = KT * D * 2;            // a K or V tile in fp16
   static constexpr int NS = D == 64 ? 8 : D == 256 && SPLIT == 2 ? 2 : 4;  // of them in the ring
@@ -40,7 +47,8 @@ struct Tc1 {
   static constexpr int ring = SPLIT * q_term;
   static constexpr int table = ring + NS * kv_tile;     // [8 warps][2][NG] float4
   static constexpr int ref = table + 8 * 2 * NG * 16;   // [128] M of O
-  static constexpr int pair = ref + kTc1Rows * 4;       // [2][128] a warpgroup's reference of its sum, sum
+  static constexpr int mem_ref = ref + kTc1Rows * 4;    // [128] M of the rows' sums in memory
+  static constexpr int pair = mem_ref + kTc1Rows * 4;       // [2][128] a warpgroup's reference of its sum, sum
   static constexpr int plan = pair + 2 * kTc1Rows * 8;  // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
   static constexpr int total = bars + (2 * NS + 10) * 8 + 16;
@@ -60,6 +68,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
   uint8_t* sQ = sm + C::q;
   uint8_t* ring = sm + C::ring;
   float* ref = reinterpret_cast<float*>(sm + C::ref);
+  float* mem_ref = reinterpret_cast<float*>(sm + C::mem_ref);
   float2* pair = reinterpret_cast<float2*>(sm + C::pair);
   int* before = reinterpret_cast<int*>(sm + C::plan);
   int* nmax = before + kMaxPlan + 1;
@@ -194,6 +203,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
+      const bool complete = count == cur.units;
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTc1Rows + row;
+      // where the row's sum goes: the output, or this CTA's piece of it
+      T* out = reinterpret_cast<T*>(a.out) + (live ? row_at() : 0);
+      float* part = a.part_o + slot * D;
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
       // exponents of a tile's 16-slot groups: lanes 0 .. NG - 1 hold one of each
@@ -285,6 +299,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
           }
           m = m1;
         }
+        if constexpr (C::flush > 0) {
+          if (i > 0 && i % C::flush == 0) {  // (the same warpgroup every time)
+            if (!wait(&pv_done[wg ^ 1], (tile - 1) >> 1)) { ok = false; break; }
+            tc_fence_after();
+            tmem_wait_st();  // O may just have been rescaled
+            // The sum keeps the reference it began with, so that adding needs no
+            // answer from memory: one thread adds to an address, in its order.  Only
+            // where that reference is not in reach the sum is read and scaled.
+            const bool begin = i == C::flush;
+            float m0 = begin ? m : mem_ref[row];
+            const bool scaled = m - m0 > 60.f || m0 == -INFINITY;
+            const float f = m0 == -INFINITY ? 0.f : fast_exp2(scaled ? m0 - m : m - m0);
+            if (begin || scaled) mem_ref[row] = m;
+            float* sum = complete ? reinterpret_cast<float*>(out) : part;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float w[16];
+              tmem_ld16(tO + c, w);
+              tmem_wait_ld();
+              if (complete && !live) continue;
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                float4* at = reinterpret_cast<float4*>(sum + c + k);
+                if (begin) {
+                  *at = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                } else if (scaled) {
+                  const float4 o = __ldcg(at);
+                  *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
+                } else {
+                  atomicAdd(at, make_float4(w[k] * f, w[k + 1] * f, w[k + 2] * f, w[k + 3] * f));
+                }
+              }
+            }
+            tc_fence_before();
+          }
+        }
         ref[row] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(&turn[wg ^ 1]);
@@ -374,7 +424,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
       }
       if (!ok) break;
       // ---- the two sums become one
-      const bool complete = count == cur.units;
       if (count > 0) {
         const int last = tile0 + count - 1;
         if ((last & 1) != wg) {  // the other warpgroup had the last word on the reference
@@ -408,16 +457,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         if (a.row_log && wg == 0) a.row_log[(int64_t)head * a.Q * a.G + rho] = log2f(l) + mx;
       }
       // ---- the item's rows, or this CTA's piece of them: half of the dims each
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTc1Rows + row;
       if (!complete && wg == 0) a.part_ml[slot] = make_float4(m, mx, l, 0.f);
-      float* part = a.part_o + slot * D;
-      T* out = reinterpret_cast<T*>(a.out) + (live ? row_at() : 0);
+      const bool in_memory = C::flush > 0 && count > C::flush;
+      const float m0 = in_memory ? mem_ref[row] : -INFINITY;
+      const float back = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
 #pragma unroll 1
       for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 16) {
         float w[16];
         if (count > 0) {
           tmem_ld16(tO + c, w);
           tmem_wait_ld();
+        }
+        if (in_memory && (live || !complete)) {
+          const float* sum = complete ? reinterpret_cast<const float*>(out) : part;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(sum + c + k));
+            w[k] = fmaf(o.x, back, w[k]);
+            w[k + 1] = fmaf(o.y, back, w[k + 1]);
+            w[k + 2] = fmaf(o.z, back, w[k + 2]);
+            w[k + 3] = fmaf(o.w, back, w[k + 3]);
+          }
         }
         if (!complete) {
 #pragma unroll
@@ -483,10 +543,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         if (!wait(&kv_full[(kv + 1) % C::NS], (kv + 1) / C::NS) || !wait(&p_full[buf], tile >> 1)) break;
         tc_fence_after();
         const uint64_t vd = sdesc_mn_sw128(rb + ((kv + 1) % C::NS) * C::kv_tile, KT * 128, 1024);
+        const bool fresh = C::flush > 0 ? i % (C::flush > 0 ? C::flush : 1) == 0 : i == 0;  // O starts here
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k) {
-            mma_f16_ts(C::colO, buf * KT + k * 8, vd + k * (2048 >> 4), idesc_pv, i > 0 || k > 0);
+            mma_f16_ts(C::colO, buf * KT + k * 8, vd + k * (2048 >> 4), idesc_pv, !fresh || k > 0);
             if constexpr (SPLIT == 2)
               mma_f16_ts(C::colO, C::colP2 + buf * (KT / 2) + k * 8, vd + k * (2048 >> 4), idesc_pv, 1);
           }

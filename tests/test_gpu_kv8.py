@@ -506,12 +506,44 @@ def test_attend_two_streams_on_one_line(d):
     assert torch.isfinite(out).all()
 
 
-def test_attend_one_tile_of_rows_a_cta():
+@pytest.mark.parametrize("d,Q,n_q,n_kv,N", [(64, 296, 64, 8, 6144), (64, 64, 14, 1, 131072), (128, 300, 64, 8, 6112),
+                                            (256, 64, 14, 1, 65536)])
+def test_attend_long_fp32_sums(d, Q, n_q, n_kv, N):
+    """fp32 prompts over so many slots that rows are summed up in parts of 2048,
+    whole items and items that CTAs share.  A part is 2048 / 16 products of two
+    terms, each truncated by 2 U at most; the parts add up rounded."""
+    B, block = 1, 32
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "f32")
+    n_vis = list(range(N - Q + 1, N + 1))
+    n_vis[Q // 2] = 0
+    clean, codes, exps, q, vis, _, _ = attend_inputs(("f32", B, Q, n_q, n_kv, d, block, N, n_vis, False, False), 91)
+    some = [0, Q // 3, Q // 2, Q - 1]
+    # one row's largest logits come late: its sum in memory is scaled down then
+    q[Q - 1] = 0.5 * q[Q - 1] + torch.from_numpy(
+        kv8.values(clean[0].numpy(), exps[0].numpy(), block)[0, :, N - 7].repeat(n_q // n_kv, 0)).float()
+    out = torch.full((Q, n_q, d), float("nan"), device=DEV)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    with rows_of_a_cta(128):
+        bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out)
+    K, V = (kv8.values(clean[i].numpy(), exps[i].numpy(), block) for i in range(2))
+    ref, _, mag, load = kv8.attend(q[some].double().numpy(), [n_vis[i] for i in some], K, V, block, d ** -0.5)
+    again = torch.full_like(out, float("nan"))
+    bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], again)
+    assert torch.equal(again, out)
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
+    within(np64(out[some]), ref, U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (512 + N / 2048 + 16) * U) * mag + 1e-30, "out")
+    # and the truncation's drift stays below 2^-18 of the output
+    got = np64(out[some])
+    assert abs((got * ref).sum() / (ref * ref).sum() - 1.0) < 2.0 ** -18
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_attend_one_tile_of_rows_a_cta(act):
     """More row tiles than one line of units holds: sequences without slots
     among them."""
     B, Q = 1030, 130
     vis = [(b * 37 + j) % 17 if b % 5 else 0 for b in range(B) for j in range(Q)]
-    check_attend(("bf16", B, Q, 1, 1, 64, 16, 16, vis, True, True), 31)
+    check_attend((act, B, Q, 1, 1, 64, 16, 16, vis, True, True), 31)
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
