@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         return (((int64_t)(head / a.H) * a.Q + rho / a.G) * a.H * a.G + head % a.H * a.G + rho % a.G) * D;
       };
       float qscale = 1.f;
+      // of a logit; never 0, which a masked slot's -inf would turn into NaN (a scale of
+      // 0, powers of two that underflow)
+      auto factor = [&](float key) { return fmaf(key, qscale, 0x1p-126f); };
       if (count > 0) {
         // ---- Q: fp16 times a power of two per row, largest magnitude in [2^14, 2^15)
         const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + (live ? row_at() : 0));
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[k] = fmaxf(fmaxf(v[16 * g + k], v[16 * g + k + 4]), fmaxf(v[16 * g + k + 8], v[16 * g + k + 12]));
-            tm = fmaxf(tm, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t.x * qscale, t.y));
+            tm = fmaxf(tm, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), factor(t.x), t.y));
           }
         }
         if (turn) {  // from here on the sum has a reference of its own
@@ -297,7 +300,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float4 t = tab[2 * hh + g];
-            const float2 c = make_float2(t.x * qscale, t.x * qscale), o = make_float2(t.y + off, t.y + off);
+            const float tc = factor(t.x);
+            const float2 c = make_float2(tc, tc), o = make_float2(t.y + off, t.y + off);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {

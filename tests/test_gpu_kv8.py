@@ -402,6 +402,30 @@ def test_attend_in_two_graphs_and_on_two_streams(act, Q, d):
         assert torch.equal(out, t[5]) and torch.equal(acc, t[4])
 
 
+@pytest.mark.parametrize("act,Q,rows", [("bf16", 3, 16), ("f32", 3, 16), ("bf16", 400, 128), ("f32", 700, 128), ("bf16", 700, 256)])
+@pytest.mark.parametrize("kind", ["scale 0", "negative scale", "underflow"])
+def test_attend_flat_and_turned_logits(act, Q, rows, kind):
+    """Logits that are all 0, by their scale or because query times key is below
+    any number, next to masked slots; and a scale below 0."""
+    B, n_q, n_kv, d, block, N = 1, 32, 4, 64, 16, 160
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    n_vis = [(7 * j) % (N + 1) for j in range(Q)]
+    clean, codes, exps, q, vis, _, _ = attend_inputs((act, B, Q, n_q, n_kv, d, block, N, n_vis, False, False), 65)
+    scale = {"scale 0": 0.0, "negative scale": -0.1, "underflow": 0.125}[kind]
+    if kind == "underflow":
+        q = (q.double() * 2.0 ** -110).to(DT[act])
+        exps[0][exps[0] != 255] = 17 + 10
+    out = torch.full_like(q, float("nan"), device=DEV)
+    dc, de = codes.to(DEV), exps.to(DEV)
+    with rows_of_a_cta(rows):
+        bd.csa_kv8_attend(p, q.to(DEV), vis.to(DEV), dc[0], de[0], dc[1], de[1], out, scale=scale)
+    e = np.where(exps.numpy() == 255, 127, exps.numpy())
+    K, V = (kv8.values(clean[i].numpy(), e[i], block) for i in range(2))
+    some = slice(0, Q, max(1, Q // 50))
+    ref, _, mag, load = kv8.attend(q[some].double().numpy(), n_vis[some], K, V, block, scale)
+    within(np64(out[some]), ref, attend_tol(act, d, N, ref, mag, load, load.max()) + 1e-30, kind)
+
+
 def test_attend_clamps_and_reports_a_length_beyond_the_cache():
     case = ("bf16", 2, 1, 4, 2, 64, 16, 64, [70, 64], False, False)
     _, codes, exps, q, _, _, _ = attend_inputs(case, 1, garbage=False)
