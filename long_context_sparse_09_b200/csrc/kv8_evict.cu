@@ -40,8 +40,8 @@ struct EvictArgs {
   int alone;  // no kv8_move: at most kFewMoves blocks go, and n_tok_out is not n_tok
 };
 
-// NaN counts as the least weight
-__device__ __forceinline__ uint32_t weight_key(float x) { return x == x ? score_key(x) : 0u; }
+// NaN counts as the least weight; -0 + 0 is 0, so the two zeros tie
+__device__ __forceinline__ uint32_t weight_key(float x) { return x == x ? score_key(x + 0.f) : 0u; }
 
 // bits set below position i
 __device__ __forceinline__ int rank_of(const uint32_t* bits, const int* before, int i) {
