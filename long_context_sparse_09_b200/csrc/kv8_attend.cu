@@ -353,6 +353,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
           }
         }
+        __syncwarp();
       }
       // ---- O += p V over codes; slots that no row sees may hold anything: the
       // item's last tile gets zeros there (whole slots, so swizzled rows too)

@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         }
         float* blk = nullptr;
         if (a.blk_log && live && vis > s0) blk = a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
+        if (a.blk_log) __syncwarp();
         if (wild) {
           // value exponents far apart: p may vanish where the sum does not
           float xm = mx;
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 #pragma unroll
             for (int k = 0; k < 16; ++k)
               if (s0 + 16 * g + k < vis) xm = fmaxf(xm, v[k] * c);
+            __syncwarp();
           }
           l *= xm > mx ? fast_exp2(mx - xm) : 1.f;
           mx = xm;
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
               if (a.sub == 16) blk[g] = log2f(sum) + mx;
               else blk[g >> 1] = log2f(held = (g & 1 ? held : 0.f) + sum) + mx;
             }
+            __syncwarp();
           }
         }
         // ---- p = 2^(y - m + 7), sums by 16 slots
@@ -325,6 +328,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
               if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
             }
           }
+          if (a.blk_log) __syncwarp();
         }
         if (!wild) l += ladd;
         tmem_wait_st();
@@ -378,6 +382,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
             *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
+          __syncwarp();
         }
       }
       tc_fence_before();

@@ -16,6 +16,9 @@ using namespace sm100;
 constexpr float kTcLazy = 8.f, kTcShift = 7.f;
 constexpr int kTcThreads = 416;  // 2 softmax warpgroups, 1 that widens, the MMA warp
 constexpr int kTcJoinRows = 16;  // rows of a join CTA
+// Loads and stores of tensor memory are the whole warp's (.sync.aligned), and rows
+// differ in what they store and see: wherever a branch on the row lies between two of
+// them, a __syncwarp() brings the lanes together again.
 
 // 16 bytes of codes (not kept in L1), or zeros
 __device__ __forceinline__ uint4 ld_stream_if(bool yes, const uint8_t* p) {

@@ -316,24 +316,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
             const float f = m0 == -INFINITY ? 0.f : fast_exp2(scaled ? m0 - m : m - m0);
             if (begin || scaled) mem_ref[row] = m;
             float* sum = complete ? reinterpret_cast<float*>(out) : part;
+            __syncwarp();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float w[16];
               tmem_ld16(tO + c, w);
               tmem_wait_ld();
-              if (complete && !live) continue;
+              if (live || !complete) {
 #pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                float4* at = reinterpret_cast<float4*>(sum + c + k);
-                if (begin) {
-                  *at = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-                } else if (scaled) {
-                  const float4 o = __ldcg(at);
-                  *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
-                } else {
-                  atomicAdd(at, make_float4(w[k] * f, w[k + 1] * f, w[k + 2] * f, w[k + 3] * f));
+                for (int k = 0; k < 16; k += 4) {
+                  float4* at = reinterpret_cast<float4*>(sum + c + k);
+                  if (begin) {
+                    *at = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                  } else if (scaled) {
+                    const float4 o = __ldcg(at);
+                    *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
+                  } else {
+                    atomicAdd(at, make_float4(w[k] * f, w[k + 1] * f, w[k + 2] * f, w[k + 3] * f));
+                  }
                 }
               }
+              __syncwarp();  // (rows differ above; the whole warp reads tensor memory)
             }
             tc_fence_before();
           }
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         if (lane == 0) mbar_arrive(&turn[wg ^ 1]);
         float* blk = nullptr;
         if (a.blk_log && live && vis > s0) blk = a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
+        if (a.blk_log) __syncwarp();
         if (wild) {
           // value exponents far apart: p may vanish where the sum does not
           float xm = mx;
@@ -355,6 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
 #pragma unroll
             for (int k = 0; k < 16; ++k)
               if (s0 + 16 * g + k < vis) xm = fmaxf(xm, v[k] * c);
+            __syncwarp();
           }
           l *= xm > mx ? fast_exp2(mx - xm) : 1.f;
           mx = xm;
@@ -373,6 +378,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
               if (a.sub == 16) blk[g] = log2f(sum) + mx;
               else blk[g >> 1] = log2f(held = (g & 1 ? held : 0.f) + sum) + mx;
             }
+            __syncwarp();
           }
         }
         // ---- p = 2^(y - m + 7), sums by 16 slots
@@ -419,6 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
               if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
             }
           }
+          if (a.blk_log) __syncwarp();
         }
         if (!wild) l += ladd;
         tmem_wait_st();
@@ -465,6 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
       const bool in_memory = C::flush > 0 && count > C::flush;
       const float m0 = in_memory ? mem_ref[row] : -INFINITY;
       const float back = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
+      __syncwarp();
 #pragma unroll 1
       for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 16) {
         float w[16];
@@ -503,6 +511,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
             *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       next_segment(u, count);

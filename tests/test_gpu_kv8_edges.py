@@ -1,4 +1,7 @@
-"""Edges of the 8-bit KV cache path."""
+"""Edges of the 8-bit KV cache path.  `attend64` is the attention in 64 bits on
+the GPU, elementary torch operations, a KV head at a time; U = 2^-24 is half a
+step of fp32.
+"""
 import numpy as np
 import pytest
 import torch
@@ -6,9 +9,54 @@ import torch
 from oracle import kv8
 from long_context_sparse_09_b200 import binding as bd
 from gpu_util import DEV
-from test_gpu_kv8 import _clean_status, random_cache  # noqa: F401
+from test_gpu_kv8 import U, _clean_status, np64, random_cache, rows_of_a_cta, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def values64(codes, exps, block):
+    """Stored values in doubles of codes [..][N][d] and exponent bytes."""
+    e = torch.exp2(exps.double() - 127.0).repeat_interleave(block, -1)
+    return codes.view(torch.float8_e4m3fn).double() * e[..., None]
+
+
+def attend64(q, n_vis, codes, exps, block, scale, sink=None):
+    """What oracle.kv8.attend returns, for tensors on the GPU: (out, weights by
+    block, sum p |v|, largest scale sum |q||k| of each row)."""
+    R, n_q, d = q.shape
+    _, B, H, N, _ = codes.shape
+    Q, G = R // B, n_q // H
+    out, mag = (torch.zeros(R, n_q, d, dtype=torch.float64, device=DEV) for _ in range(2))
+    load = torch.zeros(R, n_q, dtype=torch.float64, device=DEV)
+    w = torch.zeros(B, H, N // block, dtype=torch.float64, device=DEV)
+    step = max(1, (1 << 26) // (N * G))    # queries at a time
+    for b in range(B):
+        for h in range(H):
+            K, V = (values64(codes[i, b, h], exps[i, b, h], block) for i in range(2))
+            for j0 in range(0, Q, step):
+                r = slice(b * Q + j0, b * Q + min(Q, j0 + step))
+                at = (r, slice(h * G, (h + 1) * G))
+                x = q[at].double()
+                seen = torch.arange(N, device=DEV) < n_vis[r].clamp(0, N)[:, None, None]   # [n][1][N]
+                l = torch.where(seen, scale * (x @ K.T), -torch.inf)
+                load[at] = torch.where(seen, abs(scale) * (x.abs() @ K.abs().T), 0.0).amax(-1)
+                top = l.amax(-1, keepdim=True)
+                if sink is not None:
+                    z = sink[h * G:(h + 1) * G].double()[:, None]
+                    top = torch.maximum(top, z)
+                top = torch.where(top.isinf(), 0.0, top)
+                p = torch.exp(l - top)
+                den = p.sum(-1, keepdim=True)
+                if sink is not None:
+                    den = den + torch.exp(z - top)
+                p = torch.where(seen, p / den, 0.0)
+                out[at], mag[at] = p @ V, p @ V.abs()
+                w[b, h] += p.sum((0, 1)).view(N // block, block).sum(-1)
+    return out.cpu().numpy(), w.cpu().numpy(), mag.cpu().numpy(), load.cpu().numpy()
+
+
+def ordinary_codes(shape, g, std=60.0):
+    return (torch.randn(shape, generator=g) * std).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
 
 
 # ------------------------------------------------------------------- evict --
@@ -34,3 +82,29 @@ def test_evict_ties_of_both_zeros(NB, keep):
     for h in range(2):
         was = codes[0, 0, h].view(NB, block, d)[torch.from_numpy(ref[0, h]).long()]
         assert torch.equal(dc[0, 0, h].cpu().view(NB, block, d)[:keep], was)
+
+
+# --------------------------------------------------------- warps partly in use --
+@pytest.mark.parametrize("d,N", [(64, 6144), (128, 6112), (256, 4160)])
+def test_attend_fp32_parts_with_a_warp_partly_in_use(d, N):
+    """Whole items of more than 2048 slots (their rows are summed up in parts),
+    the last warp of a tile with 24 rows of its 32."""
+    Q, n_q, n_kv, block = 287, 64, 8, 32
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "f32")
+    assert Q * n_q // n_kv % 32 == 24 and bd.kv8_attend_workspace_bytes(p, 1, Q) == 0   # no pieces: a CTA an item
+    g = torch.Generator().manual_seed(d)
+    codes = ordinary_codes((2, 1, n_kv, N, d), g).to(DEV)
+    exps = torch.randint(115, 121, (2, 1, n_kv, N // block), generator=g, dtype=torch.uint8).to(DEV)
+    q = (2 * torch.randn(Q, n_q, d, generator=g)).to(DEV)
+    vis = torch.arange(N - Q + 1, N + 1, dtype=torch.int32, device=DEV)
+    vis[100] = 0
+    out = torch.full_like(q, float("nan"))
+    with rows_of_a_cta(128):
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out)
+    some = [0, 15, 16, 99, 100, 284, 285, 286]
+    ref, _, mag, load = attend64(q[some].contiguous(), vis[some], codes, exps, block, d ** -0.5)
+    # a part is 2048 / 16 products of two terms, each truncated by 2 U at most; the
+    # parts add up rounded
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
+    within(np64(out[some]), ref, U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (512 + N / 2048 + 16) * U) * mag + 1e-30, "out")
+    assert torch.isfinite(out).all()
