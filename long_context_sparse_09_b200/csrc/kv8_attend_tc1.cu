@@ -344,9 +344,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         ref[row] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(&turn[wg ^ 1]);
-        float* blk = nullptr;
-        if (a.blk_log && live && vis > s0) blk = a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift);
-        if (a.blk_log) __syncwarp();
+        // the row's block weights from slot s0 on
+        auto logs = [&]() { return a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift); };
         if (wild) {
           // value exponents far apart: p may vanish where the sum does not
           float xm = mx;
@@ -374,7 +373,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
             for (int k = 0; k < 16; ++k)
               if (s0 + 16 * g + k < vis) sum += fast_exp2(fmaf(v[k], c, -mx));
             l += sum;
-            if (blk && s0 + 16 * g < vis) {
+            if (a.blk_log && live && s0 + 16 * g < vis) {
+              float* blk = logs();
               if (a.sub == 16) blk[g] = log2f(sum) + mx;
               else blk[g >> 1] = log2f(held = (g & 1 ? held : 0.f) + sum) + mx;
             }
@@ -415,17 +415,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
           }
           tmem_st16(tS + hh * 16, pk);
           if constexpr (SPLIT == 2) tmem_st16(tP2 + hh * 16, pl);
-          if (blk && !wild && s0 + 32 * hh < vis) {
-            const float b0 = off + tab[2 * hh].y, b1 = off + tab[2 * hh + 1].y;
-            const bool both = s0 + 32 * hh + 16 < vis;
-            if (a.sub == 32) {
-              blk[hh] = log2f(sums[0] + (both ? sums[1] : 0.f)) - b0;
-            } else {
-              blk[2 * hh] = log2f(sums[0]) - b0;
-              if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
+          if (a.blk_log) {
+            if (live && !wild && s0 + 32 * hh < vis) {
+              float* blk = logs();
+              const float b0 = off + tab[2 * hh].y, b1 = off + tab[2 * hh + 1].y;
+              const bool both = s0 + 32 * hh + 16 < vis;
+              if (a.sub == 32) {
+                blk[hh] = log2f(sums[0] + (both ? sums[1] : 0.f)) - b0;
+              } else {
+                blk[2 * hh] = log2f(sums[0]) - b0;
+                if (both) blk[2 * hh + 1] = log2f(sums[1]) - b1;
+              }
             }
+            __syncwarp();
           }
-          if (a.blk_log) __syncwarp();
         }
         if (!wild) l += ladd;
         tmem_wait_st();
