@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(kApThreads) kv8_append_kernel(AppendArgs a) {
   cnt = min(max(cnt, 0), a.T);
   const int end = (int)min((long long)old + cnt, (long long)a.N);
   const int s0 = (old / BLOCK + bt) * BLOCK;  // first slot of this block
-  if (s0 >= end) return;
   const int lo = max(old, s0), hi = min(end, s0 + BLOCK);  // new slots [lo, hi)
+  if (lo >= hi) return;
   // (selected, not indexed: an indexed argument is copied to local memory)
   const int64_t stride = w ? a.stride[1] : a.stride[0];
   uint8_t* exps = w ? a.exps[1] : a.exps[0];

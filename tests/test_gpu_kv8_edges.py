@@ -9,7 +9,7 @@ import torch
 from oracle import kv8
 from long_context_sparse_09_b200 import binding as bd
 from gpu_util import DEV
-from test_gpu_kv8 import U, _clean_status, np64, random_cache, rows_of_a_cta, within  # noqa: F401
+from test_gpu_kv8 import DT, U, _clean_status, np64, random_cache, rows_of_a_cta, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,22 @@ def test_evict_ties_of_both_zeros(NB, keep):
     for h in range(2):
         was = codes[0, 0, h].view(NB, block, d)[torch.from_numpy(ref[0, h]).long()]
         assert torch.equal(dc[0, 0, h].cpu().view(NB, block, d)[:keep], was)
+
+
+# ------------------------------------------------------------------ append --
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_append_of_no_tokens_writes_nothing(act):
+    """Sequences without new tokens keep every byte, exponents that the library
+    would not write among them."""
+    B, T, H, d, block, N = 4, 3, 2, 64, 16, 48
+    p = bd.kv8_params(H, H, d, block, N, act)
+    codes, exps = random_cache(B, H, N, d, block, 7)
+    exps[:, :, :, 0], exps[:, :, :, 1] = 255, 3
+    dc, de = codes.to(DEV), exps.to(DEV)
+    x = torch.randn(2, B, T, H, d).to(DT[act]).to(DEV)
+    old = torch.tensor([5, 17, 32, 48], dtype=torch.int32, device=DEV)
+    bd.csa_kv8_append(p, x[0], x[1], old, dc[0], de[0], dc[1], de[1], n_new=torch.zeros_like(old))
+    assert torch.equal(dc.cpu(), codes) and torch.equal(de.cpu(), exps)
 
 
 # --------------------------------------------------------- warps partly in use --
