@@ -52,6 +52,13 @@ constexpr int kJoinUnits = 4;
 constexpr int kAccThreads = 256, kAccRows = 128, kAccFew = 32;
 constexpr float kLazy = 4.f;       // the maximum may lag by 2^4: p <= 2^15 in fp16
 constexpr float kPShift = 11.f;
+// fp32: after so many tiles a warp adds O to a sum in tensor memory and starts anew.
+// The tensor cores cut off what they add to an accumulator, towards zero: O of one
+// sign shrank by 3.6e-8 a product, 5e-5 over 128K slots; in parts by less than 4e-6.
+// It costs 1% (4 sequences of 1M, d = 128: 743 -> 747 us).  A sum in L2 cost 8%, every
+// product added to O by itself 19%.  bf16 outputs keep one accumulator: their own
+// rounding is 2^-9, a hundred times what 128K slots lose.
+constexpr int kPart = 16;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -68,6 +75,12 @@ struct Cfg {
   static constexpr int NS = D == 64 ? 3 : 2;             // tiles in a warp's ring
   static constexpr int warp_ring = NS * 2 * kv_bytes;    // (holds the warp's piece in the end: 16 rows of D + 4)
   static constexpr int steps = D / 16;
+  // fp32: columns of tensor memory, D / 2 for a warp (four warps share the columns,
+  // 32 lanes each)
+  static constexpr int tmem_cols = D == 64 ? 128 : 256;
+  // the last sum is taken up in the loop or (d = 128) by code behind it: 16 sequences
+  // of 64K, 4 KV heads, d = 256: 463 and 504 us; 4 of 1M, d = 128: 817 and 743
+  static constexpr bool fold_last = D != 128;
   static constexpr int ring = 0;
   static constexpr int qfrag = ring + NW * warp_ring;
   static constexpr int ml = qfrag + SPLIT * steps * 32 * 16;
@@ -75,13 +88,15 @@ struct Cfg {
   static constexpr int plan = rows + kRows * 8;          // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
   static constexpr int total = bars + NW * NS * 8 + 16;
+  static_assert((NW + 3) / 4 * (D / 2) <= tmem_cols, "tensor memory");
   static_assert(kRows * (D + 4) * 4 <= warp_ring && total + 1024 <= 232448, "shared memory");
 };
 
 // WEIGHTS: a CTA has the only row tile of a sequence and KV head to the end, and adds
 // its block weights up itself (a kernel of its own for it: the code would cost
 // the long walk 1%)
-template <typename T, int D, int SPLIT, bool WEIGHTS>
+// PARTS: fp32, items of more than kPart units
+template <typename T, int D, int SPLIT, bool WEIGHTS, bool PARTS>
 __global__ void __launch_bounds__(Cfg<D, SPLIT>::threads, 1)
 kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                AttnArgs a) {
@@ -97,6 +112,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   int* nmax = before + kMaxPlan + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::bars);
   volatile int* abort_sm = reinterpret_cast<volatile int*>(bars + C::NW * C::NS);
+  uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(bars + C::NW * C::NS) + 1;
   __shared__ unsigned scan_sh[33];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
@@ -112,6 +128,15 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   int e_base;
   Cursor cur;
   if (!begin_line<C::threads>(a, kRows, C::unit, before, nmax, scan_sh, cur, u0, u1, e_base)) return;
+  if constexpr (PARTS) {
+    if (warp == 0) {
+      tmem_alloc(tmem_sm, C::tmem_cols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   int issued = 0, used = 0;  // tiles of this warp so far
   uint8_t* my_ring = ring + warp * C::warp_ring;
   uint64_t* my_bars = bars + warp * C::NS;
@@ -190,11 +215,46 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    // o += the sum in tensor memory (`begin`: there is none yet), under the present
+    // reference; `away`: back there, and o starts anew
+    float m_mem[2] = {-INFINITY, -INFINITY};
+    auto add_part = [&](bool begin, bool away) {
+      const uint32_t mem = *tmem_sm + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * (D / 2);
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        f[r] = m_mem[r] == -INFINITY ? 0.f : fast_exp2(m_mem[r] - m[r]);
+        m_mem[r] = m[r];
+      }
+      __syncwarp();
+      tmem_wait_st();
+#pragma unroll
+      for (int n = 0; n < NT; n += 4) {
+        float v[16];
+        if (!begin) {
+          tmem_ld16(mem + n * 4, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[n + k / 4][k % 4] = fmaf(v[k], f[k % 4 / 2], o[n + k / 4][k % 4]);
+        }
+        if (away) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            v[k] = o[n + k / 4][k % 4];
+            o[n + k / 4][k % 4] = 0.f;
+          }
+          tmem_st16(mem + n * 4, v);
+        }
+      }
+    };
     const uint8_t* ke_p = a.k_exp + head * a.NB;
     const uint8_t* ve_p = a.v_exp + head * a.NB;
 
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0; (PARTS && C::fold_last) || i < tiles; ++i) {
+      if constexpr (PARTS)
+        if (tiles > kPart && i > 0 && (i % kPart == 0 || i == tiles)) add_part(i == kPart, i < tiles);
+      if (PARTS && C::fold_last && i >= tiles) break;
       const int s0 = first + i * C::unit;
       // exponents of the tile's two halves (a tile may end beyond the cache)
       const int i0 = s0 >> a.shift, i1 = min((s0 + 16) >> a.shift, a.NB - 1);
@@ -426,6 +486,8 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       load(i + C::NS);
     }
 
+    if constexpr (PARTS && !C::fold_last)
+      if (tiles > kPart) add_part(false, false);
     // ---- the warps' pieces become one
     u += max(count, 1);
     const bool complete = count == units;
@@ -526,6 +588,14 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     atomicOr(a.err, CSA_DEV_TIMEOUT);
     const uint64_t t0 = globaltimer();  // loads already issued land before the CTA leaves
     while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+  }
+  if constexpr (PARTS) {
+    __syncwarp();
+    tmem_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(*tmem_sm, C::tmem_cols);
   }
 }
 
@@ -733,7 +803,10 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, b
   const uint32_t box = D == 64 ? kTile / 2 : kTile;
   if (!make_tmap_bf16(&tmK, c.kc, rows, cols, box) || !make_tmap_bf16(&tmV, c.vc, rows, cols, box))
     return CSA_ERR_CUDA;
-  auto kern = weights ? kv8_attend_mma<T, D, SPLIT, true> : kv8_attend_mma<T, D, SPLIT, false>;
+  constexpr bool F32 = SPLIT == 2;
+  const bool parts = F32 && (a.N + C::unit - 1) / C::unit > kPart;
+  auto kern = parts ? (weights ? kv8_attend_mma<T, D, SPLIT, true, F32> : kv8_attend_mma<T, D, SPLIT, false, F32>)
+                    : (weights ? kv8_attend_mma<T, D, SPLIT, true, false> : kv8_attend_mma<T, D, SPLIT, false, false>);
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;

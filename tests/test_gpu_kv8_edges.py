@@ -124,3 +124,63 @@ def test_attend_fp32_parts_with_a_warp_partly_in_use(d, N):
     eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
     within(np64(out[some]), ref, U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (512 + N / 2048 + 16) * U) * mag + 1e-30, "out")
     assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------ sums over long caches --
+def drift_of(got, ref):
+    return (got * ref).sum() / (ref * ref).sum() - 1.0
+
+
+@pytest.mark.parametrize("d,H", [(64, 4), (128, 4), (256, 4)])
+def test_attend_fp32_decode_sums_do_not_drift(d, H):
+    """One query over 128K slots that one CTA walks, values of one sign: an
+    accumulator that cuts off what it adds would lose 4e-5 of them.  The rounded
+    sums stay within 2^-18, the bound that prompts have."""
+    B, N, block = 37, 131072 if d < 256 else 65536, 64
+    p = bd.kv8_params(H, H, d, block, N, "f32")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    codes = torch.randint(0x30, 0x50, (2, B, H, N, d), generator=g, device=DEV, dtype=torch.uint8)
+    exps = torch.full((2, B, H, N // block), 125, dtype=torch.uint8, device=DEV)
+    q = 0.05 * torch.randn(B, H, d, generator=g, device=DEV)
+    vis = torch.full((B,), N - 9, dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out)
+    some = [0, 17, 36]
+    ref, _, mag, load = attend64(q[some], vis[some], codes[:, some], exps[:, some], block, d ** -0.5)
+    got = np64(out[some])
+    assert abs(drift_of(got, ref)) < 2.0 ** -18, drift_of(got, ref)
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
+    # a warp's sums: N / 12 / 16 rounded steps at most (fewer warps: N / 6 / 16)
+    within(got, ref, U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (N / (96 if d == 256 else 192) + 16) * U) * mag, "out")
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_fp32_decode_parts_under_a_rising_reference(d, weights):
+    """Logits that rise with the slot: the sums of earlier parts count, scaled
+    down.  Rows of one CTA that see all slots, less than a part, and none."""
+    B, Q, H, n_q, block = 37, 2, 4, 8, 64
+    N = {64: 49152, 128: 36864, 256: 18432}[d]
+    p = bd.kv8_params(n_q, H, d, block, N, "f32")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    codes = torch.randint(0x30, 0x50, (2, B, H, N, d), generator=g, device=DEV, dtype=torch.uint8)
+    ramp = torch.linspace(-440.0, 440.0, N, device=DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes[0, ..., 0] = ramp
+    exps = torch.full((2, B, H, N // block), 125, dtype=torch.uint8, device=DEV)
+    q = 0.02 * torch.randn(B * Q, n_q, d, generator=g, device=DEV)
+    q[..., 0] = 8.0 * d ** 0.5 / 110.0    # logits from -8 to 8
+    vis = torch.full((B, Q), N - 9, dtype=torch.int32, device=DEV)
+    vis[::3, 1], vis[1::3, 0] = 1500, 0
+    vis = vis.view(-1).contiguous()
+    out = torch.empty_like(q)
+    acc = torch.zeros(B, H, N // block, device=DEV) if weights else None
+    with rows_of_a_cta(16):
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out, acc=acc)
+    some = torch.tensor([0, 1, 2, 18, 36], device=DEV)
+    rows = (some[:, None] * Q + torch.arange(Q, device=DEV)).view(-1)
+    ref, w, mag, load = attend64(q[rows], vis[rows], codes[:, some].contiguous(), exps[:, some].contiguous(), block, d ** -0.5)
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
+    within(np64(out[rows]), ref, U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (N / 96 + 16) * U) * mag, "out")
+    if weights:
+        eps = (2 * d + 16) * U * load.max() + 8 * U * load.max()
+        within(np64(acc[some]), w, (2 * eps + (N / 8 + 2 * block + 4 + 24) * U) * w + 1e-30, "acc")
