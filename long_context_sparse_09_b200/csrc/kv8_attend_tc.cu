@@ -114,11 +114,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = lanes + st * 128, tO = lanes + 256 + st * D;
     float4* table = reinterpret_cast<float4*>(sm + C::table) + warp * 64;
-    // the scale's sign goes into the queries, its power of two into their
-    // exponents, its mantissa into the keys' factors
+    // the scale's sign goes into the queries, its size into the keys' factors: there
+    // 2^-16 to 2^8 are in range whatever the exponent byte, beyond that powers of two go
+    // into the queries' exponents
     const float qsign = a.scale2 < 0.f ? -1.f : 1.f;
     const int scale_e = fabsf(a.scale2) < 0x1p-126f ? 0 : (int)(__float_as_uint(fabsf(a.scale2)) >> 23) - 127;
-    const float scale_m = fabsf(a.scale2) * pow2i(clamp_exp(-scale_e));
+    const int scale_q = scale_e - min(max(scale_e, -16), 8);
+    const float scale_k = fabsf(a.scale2) * pow2i(-scale_q);
     int tiles = 0, segment = 0, parity_o = 0;
     bool ok = true;
     for (long long u = u0; u < u1; ++segment) {
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
           }
         }
         const int qe = top ? max((int)(top >> 23) - 127 - 14, -126) : 0;
-        qscale = pow2i(clamp_exp(qe + scale_e));
+        qscale = pow2i(clamp_exp(qe + scale_q));
         const float f = pow2i(-qe) * qsign;
 #pragma unroll 2
         for (int c = 0; c < D / 8; ++c) {
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         if ((i & 3) == 0) {
           const int vl = ve - 127;
           table[(i & 4) * 8 + lane] =
-              make_float4(scale_m * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
+              make_float4(scale_k * pow2i(clamp_exp(ke - 127)), (float)vl, pow2i(clamp_exp(-vl - (int)kTcShift)), 0.f);
           turn = !wild && __any_sync(0xffffffffu, vl < -kTame || vl > kTame);
           __syncwarp();
           if (i + 4 < count) fetch(i + 4);

@@ -9,7 +9,7 @@ import torch
 from oracle import kv8
 from long_context_sparse_09_b200 import binding as bd
 from gpu_util import DEV
-from test_gpu_kv8 import DT, U, _clean_status, np64, random_cache, rows_of_a_cta, within  # noqa: F401
+from test_gpu_kv8 import DT, U, _clean_status, attend_tol, np64, random_cache, rows_of_a_cta, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +184,39 @@ def test_attend_fp32_decode_parts_under_a_rising_reference(d, weights):
     if weights:
         eps = (2 * d + 16) * U * load.max() + 8 * U * load.max()
         within(np64(acc[some]), w, (2 * eps + (N / 8 + 2 * block + 4 + 24) * U) * w + 1e-30, "acc")
+
+
+# ------------------------------------------------------- ends of fp32's range --
+FORMS = [  # act, B, Q, n_q, n_kv, d, N, rows of a CTA
+    ("bf16", 1, 3, 32, 4, 64, 160, 16), ("f32", 1, 3, 32, 4, 64, 160, 16), ("bf16", 1, 400, 32, 4, 64, 160, 128),
+    ("f32", 1, 700, 32, 4, 64, 160, 128), ("bf16", 1, 700, 32, 4, 64, 160, 256),
+    ("f32", 1, 1, 4, 2, 64, 20480, 16), ("f32", 1, 290, 14, 1, 128, 4032, 128)]
+FORM_IDS = [f"{c[0]}-Q{c[2]}-d{c[5]}-N{c[6]}-rows{c[7]}" for c in FORMS]
+
+
+def run_form(case, codes, exps, q, vis, block, scale, sink=None, acc=None, decay=1.0):
+    act, B, Q, n_q, n_kv, d, N, rows = case
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    out = torch.full((B * Q, n_q, d), float("nan"), dtype=DT[act], device=DEV)
+    ws = torch.full((bd.kv8_attend_workspace_bytes(p, B, Q, acc is not None),), 255, dtype=torch.uint8, device=DEV)
+    with rows_of_a_cta(rows):
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out, sink=sink, scale=scale, acc=acc,
+                          decay=decay, workspace=ws)
+    return out
+
+
+@pytest.mark.parametrize("case", FORMS, ids=FORM_IDS)
+def test_attend_tiny_queries_over_large_keys(case):
+    """Queries of 1e-35 and keys of 1e34: logits of a usual size."""
+    act, B, Q, n_q, n_kv, d, N, rows = case
+    g = torch.Generator().manual_seed(3)
+    block = 32
+    codes = ordinary_codes((2, B, n_kv, N, d), g).to(DEV)
+    exps = torch.randint(120, 124, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8).to(DEV)
+    exps[0] += 112
+    q = (torch.randn(B * Q, n_q, d, generator=g) * 1e-35).to(DT[act]).to(DEV)
+    vis = torch.full((B * Q,), N - 7, dtype=torch.int32, device=DEV)
+    out = run_form(case, codes, exps, q, vis, block, d ** -0.5)
+    ref, _, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5)
+    assert 1.0 < load.max() < 100.0
+    within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()), "out")
