@@ -525,11 +525,12 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         L = fmaf(v.z, v.y == -INFINITY ? 0.f : fast_exp2(v.y - MX), L);
       }
       const bool live = rho < a.Q * a.G;
-      float inv = 0.f;
+      float inv = 0.f, gap = 0.f;  // (their product may be below fp32's range where the output is not)
       const int j = rho / a.G, hq = h * a.G + rho % a.G;
       if (complete && live) {
         if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
-        inv = rowinfo[r].x > 0 ? 0x1p-11f / L * fast_exp2(M - MX) : 0.f;
+        inv = 0x1p-11f / L;
+        gap = fast_exp2(M - MX);
         if (a.row_log && tid % TPR == 0) a.row_log[head * a.Q * a.G + rho] = log2f(L) + MX;
       }
       const int64_t slot = (int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1);
@@ -551,7 +552,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           *reinterpret_cast<float4*>(part + c) = sum;
         } else if (live) {
           if (rowinfo[r].x <= 0) sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          else sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          else sum = make_float4(sum.x * inv * gap, sum.y * inv * gap, sum.z * inv * gap, sum.w * inv * gap);
           if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float4*>(out + c) = sum;
           } else {
@@ -649,12 +650,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_combine(AttnArgs a, int laun
   if (a.sink) L += fast_exp2(a.sink[hq] * kLog2e - MX);
   if (a.row_log && tid == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L) + MX;
   const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-  const float inv = 0x1p-11f / L * fast_exp2(M - MX);
+  const float inv = 0x1p-11f / L, gap = fast_exp2(M - MX);
   for (int c = tid; c < D; c += kJoinThreads) {
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < groups; ++k) t += reinterpret_cast<const float*>(&sums[k][0])[c];
-    out[c] = from_f32<T>(sees ? t * inv : 0.f);
+    out[c] = from_f32<T>(sees ? t * inv * gap : 0.f);
   }
 }
 

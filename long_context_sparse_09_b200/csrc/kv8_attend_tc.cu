@@ -345,10 +345,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
       // ---- the item's rows, or this CTA's piece of them
       const bool complete = count == cur.units;
       if (!wild) mx = m;
-      float inv = 0.f;
+      float inv = 0.f, gap = 0.f;  // (their product may be below fp32's range where the output is not)
       if (complete && live) {
         if (a.sink) l += fast_exp2(a.sink[head % a.H * a.G + rho % a.G] * kLog2e - mx);
-        if (vis > 0) inv = 0x1p-7f / l * fast_exp2(m - mx);
+        inv = 0x1p-7f / l;
+        gap = fast_exp2(m - mx);
         if (a.row_log) a.row_log[(int64_t)head * a.Q * a.G + rho] = log2f(l) + mx;
       }
       if (count > 0) {
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // (a row that sees nothing: zeros, whatever O holds)
-            const __nv_bfloat162 h2 = vis > 0 ? __floats2bfloat162_rn(w[2 * k] * inv, w[2 * k + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
+            const __nv_bfloat162 h2 = vis > 0 ? __floats2bfloat162_rn(w[2 * k] * inv * gap, w[2 * k + 1] * inv * gap) : __floats2bfloat162_rn(0.f, 0.f);
             o[k] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           if (live) {

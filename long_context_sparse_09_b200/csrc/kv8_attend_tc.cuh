@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(256) kv8_join(AttnArgs a, int launched) {
       if (a.sink) L[k] += fast_exp2(a.sink[h * a.G + (int)(rho % a.G)] * kLog2e - MX[k]);
       if (a.row_log && lane == 0) a.row_log[((int64_t)b * a.H + h) * a.Q * a.G + rho] = log2f(L[k]) + MX[k];
       const bool sees = a.n_vis[(int64_t)b * a.Q + j] > 0;
-      const float inv = 0x1p-7f / L[k] * fast_exp2(M[k] - MX[k]);
+      const float inv = 0x1p-7f / L[k], gap = fast_exp2(M[k] - MX[k]);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[k][i] = sees ? v[k][i] * inv : 0.f;
+      for (int i = 0; i < D / 32; ++i) v[k][i] = sees ? v[k][i] * inv * gap : 0.f;
     }
   }
 #pragma unroll

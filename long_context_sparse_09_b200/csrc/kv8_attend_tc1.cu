@@ -466,10 +466,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         tc_fence_after();
         tile0 += count;
       }
-      float inv = 0.f;
+      float inv = 0.f, gap = 0.f;  // (their product may be below fp32's range where the output is not)
       if (complete && live) {
         if (a.sink) l += fast_exp2(a.sink[head % a.H * a.G + rho % a.G] * kLog2e - mx);
-        if (vis > 0) inv = 0x1p-7f / l * fast_exp2(m - mx);
+        inv = 0x1p-7f / l;
+        gap = fast_exp2(m - mx);
         if (a.row_log && wg == 0) a.row_log[(int64_t)head * a.Q * a.G + rho] = log2f(l) + mx;
       }
       // ---- the item's rows, or this CTA's piece of them: half of the dims each
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
           for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(part + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
         } else if (live) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = vis > 0 ? w[k] * inv : 0.f;  // (a row that sees nothing: whatever O holds)
+          for (int k = 0; k < 16; ++k) w[k] = vis > 0 ? w[k] * inv * gap : 0.f;  // (a row that sees nothing: whatever O holds)
           if constexpr (SPLIT == 2) {
 #pragma unroll
             for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(out + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);

@@ -220,3 +220,25 @@ def test_attend_tiny_queries_over_large_keys(case):
     ref, _, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5)
     assert 1.0 < load.max() < 100.0
     within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()), "out")
+
+
+@pytest.mark.parametrize("case", FORMS, ids=FORM_IDS)
+def test_attend_tiny_values_under_a_large_sink(case):
+    """Values of 2^-100 and a sink that takes all but 2^-30: outputs are still
+    normal numbers, and as accurate as any."""
+    act, B, Q, n_q, n_kv, d, N, rows = case
+    g = torch.Generator().manual_seed(4)
+    block = 32
+    codes = ordinary_codes((2, B, n_kv, N, d), g)
+    codes[1] &= 0x7f
+    codes = codes.to(DEV)
+    exps = torch.full((2, B, n_kv, N // block), 121, dtype=torch.uint8, device=DEV)
+    exps[1] = 27
+    q = (torch.randn(B * Q, n_q, d, generator=g) * 0.1).to(DT[act]).to(DEV)
+    vis = torch.full((B * Q,), N - 7, dtype=torch.int32, device=DEV)
+    sink = torch.full((n_q,), 30.3 * np.log(2.0) + np.log(N), device=DEV)
+    out = run_form(case, codes, exps, q, vis, block, d ** -0.5, sink=sink)
+    ref, _, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5, sink)
+    # the reference of y = x - 100 rounds by 2^-18 of a power of two; sink and logits of 32
+    tol = attend_tol(act, d, N if N > 1000 else 0, ref, mag, load, load.max() + 32.0) + 2.0 ** -18 * mag
+    within(np64(out), ref, tol, "out")
