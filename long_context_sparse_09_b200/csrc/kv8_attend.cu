@@ -772,7 +772,9 @@ Way way_of(const csa_kv8_params& p, int B, int Q) {
   w.rows = w.form == kTc ? kv8_attend_tc_rows() : w.form == kTc1 ? kv8_attend_tc1_rows() : kRows;
   w.tiles = ((long long)Q * (p.n_q / p.n_kv) + w.rows - 1) / w.rows * B;
   const int unit = w.form == kMma ? mma_unit(p) : w.form == kTc1 && p.d == 256 ? 64 : 128;
-  w.planned = w.tiles <= kMaxPlan && on_a_line(w.tiles * p.n_kv, p.N, unit, kSms, w.form == kMma ? kJoinUnits : kTcJoinUnits);
+  // (the plan counts units in 32 bits)
+  w.planned = w.tiles <= kMaxPlan && w.tiles * ((p.N + (long long)unit - 1) / unit) <= 0x7fffffff &&
+              on_a_line(w.tiles * p.n_kv, p.N, unit, kSms, w.form == kMma ? kJoinUnits : kTcJoinUnits);
   return w;
 }
 
