@@ -479,8 +479,12 @@ csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, 
  *           old value is not read); blocks no query of the sequence sees are
  *           left as they are
  *   workspace / ws_bytes         >= csa_kv8_attend_workspace_bytes(with_acc =
- *           acc != NULL); 0 for calls that need none (then NULL will do).  Calls that may run at the same time need their
- *           own; nothing in it has to be kept between calls.
+ *           acc != NULL); 0 for calls that need none (then NULL will do).
+ *           Calls that may run at the same time need their own; nothing in it
+ *           has to be kept between calls.  With acc it holds 4 bytes for each
+ *           of the B Q n_q query rows and min(block, 32) slots of N; a call
+ *           that would need more than 512 MB of them runs as several, over
+ *           some of the sequences or (of one sequence) queries each.
  * Results do not depend on timing: a repeated call gives the same bits. */
 size_t csa_kv8_attend_workspace_bytes(const csa_kv8_params* p, int B, int Q, int with_acc);
 csa_status csa_kv8_attend(const csa_kv8_params* p, int B, int Q, float scale, const void* q,

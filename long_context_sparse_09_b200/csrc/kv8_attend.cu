@@ -30,6 +30,8 @@
 // waited for (issue slots 37% busy; 45% now).  One sequence of 1,111 tokens: 10 us
 // in a graph, a chain of lengths (1.2), queries (1.6), 1.5 a unit, and the join
 // of the warps (1.9).
+#include <algorithm>
+
 #include "kv8_attend.cuh"
 
 namespace csa {
@@ -726,6 +728,26 @@ __global__ void __launch_bounds__(kAccThreads) kv8_acc_join(AttnArgs a, int part
   if (seen) a.acc[at] = a.decay == 0.f ? sum : fmaf(a.decay, a.acc[at], sum);
 }
 
+// acc = decay acc for the blocks that some query of the sequence sees, before the
+// parts of a call add to it one by one
+__global__ void __launch_bounds__(kAccThreads) kv8_decay_kernel(AttnArgs a) {
+  pdl_wait();
+  __shared__ int red[kAccThreads / 32];
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int j = threadIdx.x; j < a.Q; j += kAccThreads) n = max(n, min(a.n_vis[(int64_t)b * a.Q + j], a.N));
+  n = __reduce_max_sync(0xffffffffu, n);
+  if (lane == 0) red[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = __reduce_max_sync(0xffffffffu, lane < kAccThreads / 32 ? red[lane] : 0);
+  const int i = blockIdx.x * kAccThreads + threadIdx.x;
+  if (i >= a.NB || (int64_t)i * a.block >= n) return;
+  for (int h = 0; h < a.H; ++h) {
+    float* at = a.acc + ((int64_t)b * a.H + h) * a.NB + i;
+    *at = a.decay == 0.f ? 0.f : a.decay * *at;
+  }
+}
+
 struct Ws {
   size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
 };
@@ -797,6 +819,30 @@ Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
   return w;
 }
 
+// Accumulated weights go through a number per query row and sub-block (blk_log), 4
+// bytes of workspace each: calls that would need more than this of them run as
+// several, over as many sequences or, of one sequence, queries as fit.  512 MB are two
+// milliseconds of attention (2048 queries of 64 heads over 32K slots: one call of 3.0
+// ms; as two calls 3.1, so more of them cost 2 to 5%).
+constexpr size_t kLogBytes = (size_t)512 << 20;
+struct Share {
+  int B, Q;  // sequences and queries of one call
+};
+Share share_of(const csa_kv8_params& p, int B, int Q, bool acc) {
+  const size_t query = (size_t)p.n_q * (p.N / (p.block < 32 ? p.block : 32)) * 4, seq = query * Q;
+  if (!acc || seq <= kLogBytes / B) return {B, Q};
+  if (seq <= kLogBytes) {
+    const long long most = (long long)(kLogBytes / seq), n = (B + most - 1) / most;
+    return {(int)((B + n - 1) / n), Q};
+  }
+  const long long most = query < kLogBytes ? (long long)(kLogBytes / query) : 1, n = (Q + most - 1) / most;
+  // whole tiles of 256 rows where that fits
+  long long step = kv8_attend_tc_rows();
+  for (int g = p.n_q / p.n_kv; g % 2 == 0 && step > 1; g /= 2) step /= 2;
+  const long long even = (Q + n - 1) / n, full = (even + step - 1) / step * step;
+  return {1, (int)(full <= most ? full : even)};
+}
+
 template <typename T, int D, int SPLIT>
 csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, bool weights, cudaStream_t st) {
   using C = Cfg<D, SPLIT>;
@@ -831,15 +877,8 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, b
   return ok != CSA_OK ? ok : last_launch_status();
 }
 
-}  // namespace
-
-size_t kv8_attend_ws_bytes(const csa_kv8_params& p, int B, int Q, bool acc) {
-  return layout(p, B, Q, acc).total;
-}
-
-csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale, const void* q,
-                             const int32_t* n_vis, const Kv8Cache& c, const float* sink,
-                             void* out, float* acc, float decay, void* ws, cudaStream_t st) {
+csa_status attend(const csa_kv8_params& p, int B, int Q, float scale, const void* q, const int32_t* n_vis,
+                  const Kv8Cache& c, const float* sink, void* out, float* acc, float decay, void* ws, cudaStream_t st) {
   AttnArgs a = {};
   a.q = q; a.n_vis = n_vis; a.kc = c.kc; a.vc = c.vc; a.k_exp = c.k_exp; a.v_exp = c.v_exp; a.sink = sink; a.out = out;
   a.B = B; a.Q = Q; a.H = p.n_kv; a.G = p.n_q / p.n_kv; a.N = p.N;
@@ -901,6 +940,46 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
                                     dim3(kAccThreads), 0, st, a, parts, (const float*)part) != cudaSuccess)
                  ok = CSA_ERR_CUDA);
   return ok != CSA_OK ? ok : last_launch_status();
+}
+
+}  // namespace
+
+size_t kv8_attend_ws_bytes(const csa_kv8_params& p, int B, int Q, bool acc) {
+  const Share s = share_of(p, B, Q, acc);
+  size_t most = layout(p, s.B, s.Q, acc).total;
+  if (B % s.B) most = std::max(most, layout(p, B % s.B, s.Q, acc).total);
+  if (Q % s.Q) most = std::max(most, layout(p, s.B, Q % s.Q, acc).total);
+  return most;
+}
+
+csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale, const void* q,
+                             const int32_t* n_vis, const Kv8Cache& c, const float* sink,
+                             void* out, float* acc, float decay, void* ws, cudaStream_t st) {
+  const Share s = share_of(p, B, Q, acc != nullptr);
+  if (s.Q < Q && decay != 1.f) {
+    AttnArgs a = {};
+    a.n_vis = n_vis; a.acc = acc; a.decay = decay;
+    a.Q = Q; a.H = p.n_kv; a.N = p.N; a.NB = p.N / p.block; a.block = p.block;
+    if (B > 65535) return CSA_ERR_SHAPE;
+    csa_status ok = CSA_OK;
+    CSA_LAUNCH(KK_KV8_ACC, st,
+               if (launch_maybe_pdl(true, kv8_decay_kernel, dim3((unsigned)((a.NB + kAccThreads - 1) / kAccThreads), (unsigned)B),
+                                    dim3(kAccThreads), 0, st, a) != cudaSuccess) ok = CSA_ERR_CUDA);
+    if (ok != CSA_OK) return ok;
+    decay = 1.f;
+  }
+  const int64_t row = (int64_t)p.n_q * p.d * (p.act == CSA_F32 ? 4 : 2), slots = (int64_t)p.n_kv * p.N,
+                blocks = slots / p.block;
+  for (int b = 0; b < B; b += s.B)
+    for (int j = 0; j < Q; j += s.Q) {
+      const int64_t r = (int64_t)b * Q + j;
+      const csa_status ok = attend(
+          p, std::min(s.B, B - b), std::min(s.Q, Q - j), scale, (const char*)q + r * row, n_vis + r,
+          Kv8Cache{c.kc + b * slots * p.d, c.k_exp + b * blocks, c.vc + b * slots * p.d, c.v_exp + b * blocks}, sink,
+          (char*)out + r * row, acc ? acc + b * blocks : nullptr, decay, ws, st);
+      if (ok != CSA_OK) return ok;
+    }
+  return CSA_OK;
 }
 
 }  // namespace csa

@@ -242,3 +242,48 @@ def test_attend_tiny_values_under_a_large_sink(case):
     # the reference of y = x - 100 rounds by 2^-18 of a power of two; sink and logits of 32
     tol = attend_tol(act, d, N if N > 1000 else 0, ref, mag, load, load.max() + 32.0) + 2.0 ** -18 * mag
     within(np64(out), ref, tol, "out")
+
+
+# --------------------------------------- weights of calls that run as several --
+SHARED = [
+    # act, B, Q, n_q, n_kv, d, block, N: queries of one sequence in turn (two tensor-core
+    # calls; three on mma.sync), sequences in turn
+    ("bf16", 1, 4200, 8, 1, 64, 16, 65536),
+    ("f32", 1, 70, 64, 64, 64, 16, 1 << 20),
+    ("bf16", 5, 500, 64, 8, 128, 16, 16384),
+]
+
+
+@pytest.mark.parametrize("decay", [1.0, 0.5, 0.0])
+@pytest.mark.parametrize("case", SHARED, ids=[f"{c[0]}-B{c[1]}-Q{c[2]}-N{c[7]}" for c in SHARED])
+def test_attend_weights_in_several_calls(case, decay):
+    """Each query sees more than the one before, so later calls see blocks that
+    earlier ones do not; the last blocks nobody sees."""
+    act, B, Q, n_q, n_kv, d, block, N = case
+    p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+    assert B * Q * n_q * (N // 16) * 4 > 512 << 20
+    g = torch.Generator(device=DEV).manual_seed(8)
+    codes = torch.randint(0, 0x58, (2, B, n_kv, N, d), generator=g, device=DEV, dtype=torch.uint8)
+    codes[1] += torch.randint(0, 2, codes[1].shape, generator=g, device=DEV, dtype=torch.uint8) * 0x80
+    exps = torch.full((2, B, n_kv, N // block), 121, dtype=torch.uint8, device=DEV)
+    q = (0.2 * torch.randn(B * Q, n_q, d, generator=g, device=DEV)).to(DT[act])
+    n_vis = (torch.linspace(-3, N - 4 * block - 5, Q, device=DEV).int() + 3 * torch.arange(B, device=DEV).int()[:, None])
+    n_vis = n_vis.to(torch.int32).view(-1).contiguous()
+    acc = torch.rand(B, n_kv, N // block, generator=g, device=DEV)
+    was = acc.double().cpu().numpy()
+    if decay == 0.0:
+        acc.fill_(float("nan"))
+    ws = torch.full((bd.kv8_attend_workspace_bytes(p, B, Q, True),), 255, dtype=torch.uint8, device=DEV)
+    out = torch.full((B * Q, n_q, d), float("nan"), dtype=DT[act], device=DEV)
+    bd.csa_kv8_attend(p, q, n_vis, codes[0], exps[0], codes[1], exps[1], out, acc=acc, decay=decay, workspace=ws)
+    ref, w, mag, load = attend64(q, n_vis, codes, exps, block, d ** -0.5)
+    within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()) + 1e-30, "out")
+    eps = (2 * d + 24) * U * load.max()
+    for b in range(B):
+        top = -(-int(n_vis[(b + 1) * Q - 1]) // block)
+        old = decay * was[b, :, :top] if decay else 0.0
+        # (one rounding more of the old weight, one for each call)
+        within(np64(acc[b, :, :top]), old + w[b, :, :top],
+               (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * w[b, :, :top] + 6 * U * old + 1e-30, "acc")
+        rest = np64(acc[b, :, top:])
+        assert np.isnan(rest).all() if decay == 0.0 else np.array_equal(rest, was[b, :, top:])
