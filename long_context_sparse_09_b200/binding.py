@@ -636,11 +636,20 @@ def _launch(name, dev, stream, *args):
         _check(name, st)
 
 
+def _empty_on(stream, n, dtype, device):
+    """Memory that belongs to the call's stream: what the current stream still
+    has to do with a block that was freed there must not meet the call."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 def csa_rope_freqs(rope: CsaRope, device="cuda", stream=None) -> torch.Tensor:
     """The fp64 table [rope_dims/2] of turns per token that csa_qk_norm_rope reads."""
-    turns = torch.empty(rope.rope_dims // 2, dtype=torch.float64, device=device)
-    if stream is not None:
-        turns.record_stream(stream)
+    turns = _empty_on(stream, rope.rope_dims // 2, torch.float64, device)
+    if stream is not None:   # the caller's stream will read it
+        turns.record_stream(torch.cuda.current_stream(turns.device))
     _launch("csa_rope_freqs", _cuda_dev(turns, "turns"), stream, C.byref(rope), turns.data_ptr() or None)
     return turns
 
@@ -737,9 +746,7 @@ def csa_kv8_attend(p: CsaKv8Params, q, n_vis, kc, k_exp, vc, v_exp, out, sink=No
     wp, wb = None, 0
     if need:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _empty_on(stream, need, torch.uint8, q.device)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous tensor on cuda:{dev} expected")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -287,3 +287,43 @@ def test_attend_weights_in_several_calls(case, decay):
                (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * w[b, :, :top] + 6 * U * old + 1e-30, "acc")
         rest = np64(acc[b, :, top:])
         assert np.isnan(rest).all() if decay == 0.0 else np.array_equal(rest, was[b, :, top:])
+
+
+# ------------------------------------------------------- a stream of their own --
+def test_calls_on_another_stream_take_no_memory_in_use():
+    """Memory that was freed on the current stream may still be written there:
+    what a call on another stream allocates must not be that memory."""
+    s = torch.cuda.Stream()
+    rope = bd.rope_params(128, 64)
+    want = bd.csa_rope_freqs(rope)
+    p = bd.kv8_params(8, 2, 64, 16, 20480, "bf16")
+    need = bd.kv8_attend_workspace_bytes(p, 1, 1)
+    codes, exps = random_cache(1, 2, 20480, 64, 16, 3)
+    codes, exps = codes.to(DEV), exps.to(DEV)
+    q = torch.randn(1, 8, 64, device=DEV).to(torch.bfloat16)
+    vis = torch.tensor([20001], dtype=torch.int32, device=DEV)
+    ref, out = torch.empty_like(q), torch.empty_like(q)
+    bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], ref)
+    torch.cuda.synchronize()
+    freed = torch.empty(32, dtype=torch.float64, device=DEV), torch.empty(need, dtype=torch.uint8, device=DEV)
+    at = [t.data_ptr() for t in freed]
+    torch.cuda._sleep(200_000_000)   # a tenth of a second
+    for t in freed:
+        t.fill_(255)
+    del freed, t
+    taken = []
+    empty = torch.empty
+
+    def watched(*args, **kw):
+        t = empty(*args, **kw)
+        taken.append(t.data_ptr())
+        return t
+    torch.empty = watched
+    try:
+        got = bd.csa_rope_freqs(rope, stream=s)
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out, stream=s)
+    finally:
+        torch.empty = empty
+    assert len(taken) == 2 and not set(taken) & set(at)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(out, ref)
