@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
   volatile int* abort_sm = reinterpret_cast<volatile int*>(s_full + 10);
   uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(s_full + 10) + 1;
   __shared__ unsigned scan_sh[33];
+  __shared__ int wild_sm[4];  // by 32 rows: the last segment (from 1) with value exponents far apart
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid < 4) wild_sm[tid] = 0;
   if (tid == 0) {
     *abort_sm = 0;
     for (int i = 0; i < C::NS; ++i) {
@@ -215,6 +217,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
       float* part = a.part_o + slot * D;
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
+      // The reference that the other warpgroup left, m0 >= m.  Value exponents far apart
+      // that only its tiles hold may have lifted it: this one's sum, which is of x, then
+      // keeps a reference of its own as well (under m0 it could vanish, next to the
+      // least of exp2_poly).
+      auto follow = [&]() {
+        const float m0 = ref[row];
+        if (!wild && wild_sm[warp & 3] == segment + 1) {
+          wild = true;
+          mx = m;
+        }
+        if (m0 != m) {  // (m0 > m; m = -inf: l is 0)
+          if (!wild) l *= fast_exp2(m - m0);
+          m = m0;
+        }
+      };
       // exponents of a tile's 16-slot groups: lanes 0 .. NG - 1 hold one of each
       int ke = 127, ve = 127;
       auto fetch = [&](int i) {
@@ -274,15 +291,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         if (far) {  // from here on the sum has a reference of its own
           wild = true;
           mx = m;
+          if (lane == 0) wild_sm[warp & 3] = segment + 1;
         }
         // ---- the reference that the other warpgroup left with the tile before
         if (i > 0) {
           if (!wait(&turn[wg], turns++)) { ok = false; break; }
-          const float m0 = ref[row];
-          if (m0 != m) {  // (m0 > m; m = -inf: l is 0)
-            if (!wild) l *= fast_exp2(m - m0);
-            m = m0;
-          }
+          follow();
         }
         if (__any_sync(0xffffffffu, tm > m + kTcLazy)) {
           const float m1 = fmaxf(m, tm);
@@ -444,11 +458,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
         const int last = tile0 + count - 1;
         if ((last & 1) != wg) {  // the other warpgroup had the last word on the reference
           if (!wait(&turn[wg], turns++)) break;
-          const float m0 = ref[row];
-          if (m0 != m) {
-            if (!wild) l *= fast_exp2(m - m0);
-            m = m0;
-          }
+          follow();
         }
         if (!wild) mx = m;
         pair[wg * kTc1Rows + row] = make_float2(mx, l);

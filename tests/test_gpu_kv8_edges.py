@@ -327,3 +327,48 @@ def test_calls_on_another_stream_take_no_memory_in_use():
     assert len(taken) == 2 and not set(taken) & set(at)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(out, ref)
+
+
+# ---------------------------------------------- value exponents far apart, by form --
+FAR = [  # act, B, Q, n_q, n_kv, d, block, N, rows of a CTA
+    ("bf16", 2, 210, 48, 8, 64, 16, 1296, 256), ("bf16", 1, 300, 64, 8, 64, 64, 1280, 256),
+    ("bf16", 1, 300, 64, 8, 128, 16, 1296, 256), ("bf16", 2, 210, 48, 8, 128, 32, 1312, 256),
+    ("bf16", 1, 480, 14, 1, 128, 32, 16384, 256),
+    ("bf16", 1, 290, 14, 1, 128, 32, 2016, 128), ("bf16", 1, 150, 64, 8, 256, 16, 1296, 128),
+    ("f32", 1, 150, 64, 8, 128, 16, 1296, 128), ("f32", 1, 300, 48, 6, 256, 64, 1280, 128)]
+KINDS = ["zeros first", "zeros between", "far apart", "far from 200", "far from 700", "far from 1100"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", FAR, ids=[f"{c[0]}-d{c[5]}-blk{c[6]}-N{c[7]}-rows{c[8]}" for c in FAR])
+def test_attend_value_exponents_far_apart_by_form(case, kind):
+    """Logits do not depend on the values' exponents, so neither may weights; the
+    first block out of the ordinary lies in any tile of a group of four, or in a
+    later group."""
+    act, B, Q, n_q, n_kv, d, block, N, rows = case
+    g = torch.Generator().manual_seed(N + d)
+    codes = ordinary_codes((2, B, n_kv, N, d), g)
+    exps = torch.randint(115, 121, (2, B, n_kv, N // block), generator=g, dtype=torch.uint8)
+    i = torch.arange(N // block)
+    if kind.startswith("zeros"):
+        zero = i < 3 * len(i) // 4 if kind == "zeros first" else i % 3 == 1
+        codes[1].view(B, n_kv, -1, block, d)[:, :, zero] = 0
+        exps[1][:, :, zero] = 17
+    else:
+        far = i * block >= (0 if kind == "far apart" else int(kind.split()[-1]) * N // 1280)
+        wild = torch.tensor([17, 70, 127, 190, 246], dtype=torch.uint8)
+        exps[1][:, :, far] = wild[torch.randint(0, 5, (B, n_kv, int(far.sum())), generator=g)]
+    q = (2 * torch.randn(B * Q, n_q, d, generator=g)).to(DT[act]).to(DEV)
+    vis = torch.from_numpy(np.random.default_rng(N).integers(N // 2, N + 1, B * Q).astype(np.int32))
+    vis[5], vis[6], vis[7] = 0, 1, N // 3
+    codes, exps, vis = codes.to(DEV), exps.to(DEV), vis.to(DEV)
+    acc = torch.zeros(B, n_kv, N // block, device=DEV)
+    out = run_form((act, B, Q, n_q, n_kv, d, N, rows), codes, exps, q, vis, block, d ** -0.5, acc=acc)
+    ref, w, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5)
+    rng = load.max()
+    # a term 2^7 2^(y - M) in fp16 is off by half its least step, 2^-25, at most where it is
+    # subnormal: 2^-32 of the largest weight times 2^exponent, for each of N slots' codes up to 448
+    top = 0.0 if kind.startswith("zeros") else N * 2.0 ** -32 * 448.0 * 2.0 ** (float(exps[1].max()) - 127.0)
+    within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, rng) + top + 1e-36, "out")
+    eps = (2 * d + 24) * U * rng
+    within(np64(acc), w, (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * w + 1e-30, "acc")
