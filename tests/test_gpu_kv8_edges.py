@@ -372,3 +372,60 @@ def test_attend_value_exponents_far_apart_by_form(case, kind):
     within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, rng) + top + 1e-36, "out")
     eps = (2 * d + 24) * U * rng
     within(np64(acc), w, (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * w + 1e-30, "acc")
+
+
+# ------------------------------------------- sums in parts whose reference leaps --
+LEAP = [  # Q, n_q, n_kv, d, N, leaps at: whole items, and items that CTAs share
+    (287, 64, 8, 64, 12288, (5000, 9000)), (287, 64, 8, 128, 12288, (4500, 9900)),
+    (287, 64, 8, 256, 12288, (5300, 8300)), (64, 14, 1, 64, 131072, (60000, 100000)),
+    (64, 14, 1, 128, 131072, (30000, 34000))]
+
+
+@pytest.mark.parametrize("case", LEAP, ids=[f"d{c[3]}-N{c[4]}" for c in LEAP])
+def test_attend_fp32_parts_when_the_reference_leaps(case):
+    """Prompts of fp32 activations keep a row's sum of parts of 2048 slots in memory
+    under the reference it began with; a rise beyond 2^60 scales that sum.  Every third
+    query meets two such rises, one in a later part and one after that: the slots
+    that cause them have no value in a third of the dims and only the first has
+    one in another third, so that what was scaled down once and twice can be read
+    off."""
+    Q, n_q, n_kv, d, N, leaps = case
+    block, tile = 32, 64 if d == 256 else 128
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "f32")
+    g = torch.Generator().manual_seed(d + N)
+    codes = torch.randint(0x30, 0x50, (2, 1, n_kv, N, d), generator=g, dtype=torch.uint8)
+    codes[0] += torch.randint(0, 2, codes[0].shape, generator=g, dtype=torch.uint8) * 0x80
+    level = torch.zeros(N)                       # logits of the leaping queries, in powers of two
+    level[leaps[0] // tile * tile:] = -32.0      # what follows does not count
+    level[leaps[0]], level[leaps[1]] = 64.0, 128.0
+    codes[0, 0, :, :, 0] = level.to(torch.float8_e4m3fn).view(torch.uint8)
+    codes[1, 0, :, leaps[0], 0::3] = 0
+    codes[1, 0, :, leaps[1], 0::3] = 0
+    codes[1, 0, :, leaps[1], 1::3] = 0
+    exps = torch.full((2, 1, n_kv, N // block), 127, dtype=torch.uint8)
+    exps[1] += 20
+    q = 0.1 * torch.randn(Q, n_q, d, generator=g)
+    q[..., 0] = 0.0
+    q[::3, :, 0] = 1.1 * np.log(2.0) * d ** 0.5
+    vis = torch.full((Q,), N - 3, dtype=torch.int32)
+    vis[1] = leaps[0] + 40
+    codes, exps, q, vis = codes.to(DEV), exps.to(DEV), q.to(DEV), vis.to(DEV)
+    # the rises, from the logits in 64 bits
+    K = values64(codes[0, 0, 0], exps[0, 0, 0], block)
+    y = (q[0, :n_q // n_kv].double() @ K.T) * d ** -0.5 / np.log(2.0)
+    steps = [y[:, :n].amax(-1) for n in (2048, leaps[0], leaps[0] + 1, leaps[1], leaps[1] + 1)]
+    assert (steps[1] - steps[0]).max() < 8 and (steps[2] - steps[1]).min() > 60
+    assert (steps[3] - steps[2]).max() == 0 and (steps[4] - steps[3]).min() > 60
+    out = torch.full_like(q, float("nan"))
+    with rows_of_a_cta(128):
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out)
+    some = [0, 1, 2, 3, 30, Q // 3 * 3 - 3, Q - 1]
+    ref, _, mag, load = attend64(q[some].contiguous(), vis[some], codes, exps, block, d ** -0.5)
+    eps = (2 * d + 16) * U * load[..., None] + 8 * U * load.max()
+    tol = U * np.abs(ref) + (2 * eps + 2.0 ** -22 + (512 + N / 2048 + 16) * U) * mag
+    if Q == 64:   # pieces that lie more than 2^126 below the largest one are joined with a
+        # factor of 0 (fp32 has no normal number there): N weights below 2^-126 of values
+        # up to 448 2^20
+        tol = tol + N * 2.0 ** -126 * 448 * 2.0 ** 20
+    within(np64(out[some]), ref, tol, "out")
+    assert torch.isfinite(out).all()
