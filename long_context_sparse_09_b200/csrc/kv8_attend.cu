@@ -60,7 +60,7 @@ constexpr float kPShift = 11.f;
 // It costs 1% (4 sequences of 1M, d = 128: 743 -> 747 us).  A sum in L2 cost 8%, every
 // product added to O by itself 19%.  bf16 outputs keep one accumulator: their own
 // rounding is 2^-9, a hundred times what 128K slots lose.
-constexpr int kPart = 16;
+constexpr int kPart = 16, kPartBf16 = 512;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -97,12 +97,13 @@ struct Cfg {
 // WEIGHTS: a CTA has the only row tile of a sequence and KV head to the end, and adds
 // its block weights up itself (a kernel of its own for it: the code would cost
 // the long walk 1%)
-// PARTS: fp32, items of more than kPart units
+// PARTS: a CTA may walk more than PT units of an item
 template <typename T, int D, int SPLIT, bool WEIGHTS, bool PARTS>
 __global__ void __launch_bounds__(Cfg<D, SPLIT>::threads, 1)
 kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                AttnArgs a) {
   using C = Cfg<D, SPLIT>;
+  constexpr int PT = SPLIT == 2 ? kPart : kPartBf16;
   constexpr int NT = D / 8;  // output n-tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -255,7 +256,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll 1
     for (int i = 0; (PARTS && C::fold_last) || i < tiles; ++i) {
       if constexpr (PARTS)
-        if (tiles > kPart && i > 0 && (i % kPart == 0 || i == tiles)) add_part(i == kPart, i < tiles);
+        if (tiles > PT && i > 0 && (i % PT == 0 || i == tiles)) add_part(i == PT, i < tiles);
       if (PARTS && C::fold_last && i >= tiles) break;
       const int s0 = first + i * C::unit;
       // exponents of the tile's two halves (a tile may end beyond the cache)
@@ -489,7 +490,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
 
     if constexpr (PARTS && !C::fold_last)
-      if (tiles > kPart) add_part(false, false);
+      if (tiles > PT) add_part(false, false);
     // ---- the warps' pieces become one
     u += max(count, 1);
     const bool complete = count == units;
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kAccThreads) kv8_decay_kernel(AttnArgs a) {
 }
 
 struct Ws {
-  size_t plan, part_ml, part_o, row_log, acc_part, blk_log, total;
+  size_t plan, part_ml, part_o, sum_o, row_log, acc_part, blk_log, total;
 };
 
 int mma_unit(const csa_kv8_params& p) {  // slots of a unit here
@@ -787,6 +788,7 @@ struct Way {
   int rows;         // query rows of a CTA
   long long tiles;  // (sequence, row tile) pairs
   bool planned;     // the units of all items on one line
+  bool parts;       // a CTA may walk so many slots of an item that O is summed up in parts
 };
 Way way_of(const csa_kv8_params& p, int B, int Q) {
   Way w;
@@ -794,9 +796,16 @@ Way way_of(const csa_kv8_params& p, int B, int Q) {
   w.rows = w.form == kTc ? kv8_attend_tc_rows() : w.form == kTc1 ? kv8_attend_tc1_rows() : kRows;
   w.tiles = ((long long)Q * (p.n_q / p.n_kv) + w.rows - 1) / w.rows * B;
   const int unit = w.form == kMma ? mma_unit(p) : w.form == kTc1 && p.d == 256 ? 64 : 128;
+  const bool f32 = p.act == CSA_F32;
+  const long long per = (p.N + (long long)unit - 1) / unit, items = w.tiles * p.n_kv;
+  // of the tensor-core forms' bf16 sums, whose memory goes by CTA (share_of sees to it
+  // that such calls fit a plan)
+  const bool sums = w.form != kMma && !f32 && p.N > kPartSlots;
   // (the plan counts units in 32 bits)
-  w.planned = w.tiles <= kMaxPlan && w.tiles * ((p.N + (long long)unit - 1) / unit) <= 0x7fffffff &&
-              on_a_line(w.tiles * p.n_kv, p.N, unit, kSms, w.form == kMma ? kJoinUnits : kTcJoinUnits);
+  w.planned = w.tiles <= kMaxPlan && w.tiles * per <= 0x7fffffff &&
+              (sums || on_a_line(items, p.N, unit, kSms, w.form == kMma ? kJoinUnits : kTcJoinUnits));
+  const long long longest = w.planned ? std::min(per, items * per / kSms + 1) : per;
+  w.parts = w.form == kMma ? longest > (f32 ? kPart : kPartBf16) : sums && w.planned && longest > kPartSlots / unit;
   return w;
 }
 
@@ -811,7 +820,8 @@ Ws layout(const csa_kv8_params& p, int B, int Q, bool acc) {
   w.plan = 0;
   w.part_ml = w.plan + (way.planned ? align_up((kMaxPlan + 1) * 4, 256) : 0);
   w.part_o = w.part_ml + pieces * 16;
-  w.row_log = w.part_o + pieces * p.d * 4;
+  w.sum_o = w.part_o + pieces * p.d * 4;
+  w.row_log = w.sum_o + (way.parts && way.form != kMma ? (size_t)kMaxGrid * way.rows * p.d * 4 : 0);
   w.acc_part = w.row_log + (acc ? align_up(rows * 4, 256) : 0);
   const int parts = acc_parts(p, Q);
   w.blk_log = w.acc_part + (acc && parts > 1 ? align_up((size_t)parts * B * p.n_kv * (p.N / p.block) * 4, 256) : 0);
@@ -828,7 +838,7 @@ constexpr size_t kLogBytes = (size_t)512 << 20;
 struct Share {
   int B, Q;  // sequences and queries of one call
 };
-Share share_of(const csa_kv8_params& p, int B, int Q, bool acc) {
+Share log_share(const csa_kv8_params& p, int B, int Q, bool acc) {
   const size_t query = (size_t)p.n_q * (p.N / (p.block < 32 ? p.block : 32)) * 4, seq = query * Q;
   if (!acc || seq <= kLogBytes / B) return {B, Q};
   if (seq <= kLogBytes) {
@@ -843,6 +853,19 @@ Share share_of(const csa_kv8_params& p, int B, int Q, bool acc) {
   return {1, (int)(full <= most ? full : even)};
 }
 
+// bf16 prompts over so many slots that O is summed up in parts: those sums have memory
+// for the CTAs of a plan, so row tiles that no plan holds go into calls of their own
+// (of a tenth of a second and more).
+Share share_of(const csa_kv8_params& p, int B, int Q, bool acc) {
+  Share s = log_share(p, B, Q, acc);
+  if (p.act == CSA_F32 || p.N <= kPartSlots || way_of(p, s.B, s.Q).form == kMma) return s;
+  const long long rows = kv8_attend_tc1_rows(), G = p.n_q / p.n_kv;
+  const long long most = std::min((long long)kMaxPlan, 0x7fffffffll / ((p.N + 63) / 64)), tiles = (s.Q * G + rows - 1) / rows;
+  if (tiles <= most) s.B = (int)std::min((long long)s.B, most / tiles);
+  else s.B = 1, s.Q = (int)std::max(1ll, most * rows / G);
+  return s;
+}
+
 template <typename T, int D, int SPLIT>
 csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, bool weights, cudaStream_t st) {
   using C = Cfg<D, SPLIT>;
@@ -852,10 +875,8 @@ csa_status launch_mma(const csa_kv8_params& p, const Kv8Cache& c, AttnArgs& a, b
   const uint32_t box = D == 64 ? kTile / 2 : kTile;
   if (!make_tmap_bf16(&tmK, c.kc, rows, cols, box) || !make_tmap_bf16(&tmV, c.vc, rows, cols, box))
     return CSA_ERR_CUDA;
-  constexpr bool F32 = SPLIT == 2;
-  const bool parts = F32 && (a.N + C::unit - 1) / C::unit > kPart;
-  auto kern = parts ? (weights ? kv8_attend_mma<T, D, SPLIT, true, F32> : kv8_attend_mma<T, D, SPLIT, false, F32>)
-                    : (weights ? kv8_attend_mma<T, D, SPLIT, true, false> : kv8_attend_mma<T, D, SPLIT, false, false>);
+  auto kern = a.parts ? (weights ? kv8_attend_mma<T, D, SPLIT, true, true> : kv8_attend_mma<T, D, SPLIT, false, true>)
+                      : (weights ? kv8_attend_mma<T, D, SPLIT, true, false> : kv8_attend_mma<T, D, SPLIT, false, false>);
   const int smem = C::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
@@ -892,6 +913,7 @@ csa_status attend(const csa_kv8_params& p, int B, int Q, float scale, const void
   a.E = (int)way.tiles;
   a.RT = a.E / B;
   a.planned = way.planned;
+  a.parts = way.parts;
   const bool few = (long long)Q * a.G <= kAccFew;
   const int tiles = (a.NSB + (few ? kAccThreads : 32) - 1) / (few ? kAccThreads : 32), parts = acc_parts(p, Q);
   const long long blocks = (long long)B * a.H * a.NB;
@@ -907,6 +929,7 @@ csa_status attend(const csa_kv8_params& p, int B, int Q, float scale, const void
   a.plan = (int*)(base + w.plan);
   a.part_ml = (float4*)(base + w.part_ml);
   a.part_o = (float*)(base + w.part_o);
+  a.sum_o = (float4*)(base + w.sum_o);
   if (acc) {
     a.acc = acc;
     a.row_log = (float*)(base + w.row_log);
@@ -956,7 +979,7 @@ csa_status launch_kv8_attend(const csa_kv8_params& p, int B, int Q, float scale,
                              const int32_t* n_vis, const Kv8Cache& c, const float* sink,
                              void* out, float* acc, float decay, void* ws, cudaStream_t st) {
   const Share s = share_of(p, B, Q, acc != nullptr);
-  if (s.Q < Q && decay != 1.f) {
+  if (acc && s.Q < Q && decay != 1.f) {
     AttnArgs a = {};
     a.n_vis = n_vis; a.acc = acc; a.decay = decay;
     a.Q = Q; a.H = p.n_kv; a.N = p.N; a.NB = p.N / p.block; a.block = p.block;

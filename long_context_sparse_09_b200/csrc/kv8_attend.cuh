@@ -24,6 +24,11 @@ constexpr int kMaxGrid = 160;      // CTAs whose pieces the workspace holds (148
 // overflow nor lose a term of weight.  Where a sequence has others (blocks of
 // zeros, above all), its sum gets a maximum of its own, that of x.
 constexpr int kTame = 40;
+// The tensor cores cut off what they add to an accumulator, towards zero, and of
+// products far below it all but a few bits.  bf16 prompts over values of one sign lost
+// 1.3e-4 over 32K slots, 9e-4 over 128K and 8e-3 over 1M: after so many slots of an
+// item O goes to a sum in memory and starts anew (0.8% of the time).
+constexpr int kPartSlots = 32768;
 
 struct AttnArgs {
   const void* q;
@@ -37,6 +42,7 @@ struct AttnArgs {
   float* blk_log;   // [B][H][Q G][NSB] log2 of each sub-block's weight sum (not normalised)
   float* row_log;   // [B][H][Q G] log2 of the row's denominator
   float* part_o;    // [grid][2][rows of a CTA][d] pieces of items that several CTAs share
+  float4* sum_o;    // tensor-core forms, bf16, in parts: [grid][rows of a CTA][d] floats
   float4* part_ml;  // [grid][2][rows of a CTA] their M, reference of the sum, sum
   int* plan;        // [E + 1] units before each (sequence, row tile)
   float* acc;
@@ -45,6 +51,7 @@ struct AttnArgs {
   int sub, NSB;     // slots of a sub-block: min(block, 32); sub-blocks of N
   int shift, sub_shift;  // log2 of block and sub
   int RT, E, planned;
+  int parts;        // O is summed up in parts (its CTAs may walk so many slots of an item)
   float scale2, decay;  // softmax scale times log2(e)
 };
 

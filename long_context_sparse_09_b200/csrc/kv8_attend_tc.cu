@@ -49,16 +49,21 @@ struct Tc {
   static constexpr int table = ring + NS * row_tile;           // [8 warps][2][32] float4
   static constexpr int plan = table + 8 * 2 * 32 * 16;         // units before, n_max: [E + 1], [E]
   static constexpr int bars = plan + (2 * kMaxPlan + 2) * 4;
-  static constexpr int total = bars + (2 * NS + 8) * 8 + 16;
+  static constexpr int mem_ref = bars + (2 * NS + 8) * 8 + 16;  // [256] M of the rows' sums in memory
+  static constexpr int total = mem_ref + kTcRows * 4;
+  static_assert(total + 1024 <= 232448, "shared memory");
 };
 
-template <int D>
+// PARTS: CTAs may walk more than kPartSlots slots of an item
+template <int D, bool PARTS>
 __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a) {
   using C = Tc<D>;
+  constexpr int kPart = kPartSlots / kTcTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = sm + C::q;
   uint8_t* ring = sm + C::ring;
+  float* mem_ref = reinterpret_cast<float*>(sm + C::mem_ref);
   int* before = reinterpret_cast<int*>(sm + C::plan);
   int* nmax = before + kMaxPlan + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::bars);
@@ -173,6 +178,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[st]);
       }
+      // the row's sum in memory, dims c to c + 3 (a warp's rows side by side)
+      auto sum_at = [&](int c) { return a.sum_o + ((int64_t)blockIdx.x * (D / 4) + c / 4) * kTcRows + st * 128 + row; };
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
       // exponents of the 16-slot groups of four tiles, a lane one of each; their
@@ -255,6 +262,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
             }
           }
           m = m1;
+        }
+        if constexpr (PARTS) {
+          if (i > 0 && i % kPart == 0) {  // (S is there: the P V before it is done)
+            const bool begin = i == kPart;
+            const float m0 = begin ? -INFINITY : mem_ref[st * 128 + row];
+            const float f = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
+            mem_ref[st * 128 + row] = m;
+            __syncwarp();
+            tmem_wait_st();  // O may just have been rescaled
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float w[16];
+              tmem_ld16(tO + c, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                float4* at = sum_at(c + k);
+                const float4 o = begin ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(at);
+                *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
+              }
+            }
+          }
         }
         // the row's block weights from slot s0 on
         auto logs = [&]() { return a.blk_log + ((int64_t)head * a.Q * a.G + rho) * a.NSB + (s0 >> a.sub_shift); };
@@ -357,6 +386,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
         ++parity_o;
         tc_fence_after();
       }
+      const bool in_memory = PARTS && count > kPart;
+      const float back = in_memory && mem_ref[st * 128 + row] != -INFINITY ? fast_exp2(mem_ref[st * 128 + row] - m) : 0.f;
+      auto take_up = [&](int c, float (&w)[16]) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const float4 o = __ldcg(sum_at(c + k));
+          w[k] = fmaf(o.x, back, w[k]);
+          w[k + 1] = fmaf(o.y, back, w[k + 1]);
+          w[k + 2] = fmaf(o.z, back, w[k + 2]);
+          w[k + 3] = fmaf(o.w, back, w[k + 3]);
+        }
+      };
+      __syncwarp();
       if (!complete) {
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (segment == 0 ? 0 : 1)) * kTcRows + st * 128 + row;
         a.part_ml[slot] = make_float4(m, mx, l, 0.f);
@@ -366,6 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
           float w[16];
           tmem_ld16(tO + c, w);
           tmem_wait_ld();
+          if (PARTS && in_memory) take_up(c, w);
 #pragma unroll
           for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(part + c + k) = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
         }
@@ -378,6 +421,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
             tmem_ld16(tO + c, w);
             tmem_wait_ld();
           }
+          if (PARTS && in_memory) take_up(c, w);
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // (a row that sees nothing: zeros, whatever O holds)
@@ -439,6 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 #pragma unroll 1
       for (int i = 0; ok && i < count; ++i, ++tiles, kv += 2) {
         const uint64_t vd = sdesc_mn_sw128(rb + ((kv + 1) % C::NS) * C::row_tile, 16384, 1024);
+        const bool fresh = PARTS ? i % kPart == 0 : i == 0;  // O starts here
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s == 0) wait_kv(kv + 1);
@@ -447,7 +492,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kTcTile / 16; ++k)
-              mma_f16_ts(256 + s * D, s * 128 + k * 8, vd + k * (2048 >> 4), idesc_pv, i > 0 || k > 0);
+              mma_f16_ts(256 + s * D, s * 128 + k * 8, vd + k * (2048 >> 4), idesc_pv, !fresh || k > 0);
             if (s == 1) mma_commit(&kv_empty[(kv + 1) % C::NS]);
             if (i + 1 == count) mma_commit(&o_full[s]);
           }
@@ -476,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
 
 template <int D>
 csa_status launch_tc(AttnArgs& a, cudaStream_t st) {
-  auto kern = kv8_attend_tc_kernel<D>;
+  auto kern = a.parts ? kv8_attend_tc_kernel<D, true> : kv8_attend_tc_kernel<D, false>;
   const int smem = Tc<D>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kTc1Rows = 128;  // query rows of a CTA
 
-template <typename T, int D>
+template <typename T, int D, bool PARTS>
 struct Tc1 {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of q and p
   static constexpr int KT = D == 256 ? 64 : 128;        // slots of a tile
@@ -39,7 +39,8 @@ struct Tc1 {
   // accumulator, always towards zero: over 16K slots O shrank by 1.4e-5 (relative
   // error 1.7e-5; with the parts 4.4e-6, with parts of 1024 slots 3.1e-6, plain fp32
   // torch 2.6e-6).  It costs 14% (d = 128; parts of 1024: 24%).
-  static constexpr int flush = SPLIT == 2 ? 2048 / KT : 0;
+  // bf16: where CTAs may walk more than kPartSlots slots of an item, after those.
+  static constexpr int flush = SPLIT == 2 ? 2048 / KT : PARTS ? kPartSlots / KT : 0;
   static constexpr int q_term = kTc1Rows * D * 2;       // a term of the queries
   static constexpr int kv_tile = KT * D * 2;            // a K or V tile in fp16
   static constexpr int NS = D == 64 ? 8 : D == 256 && SPLIT == 2 ? 2 : 4;  // of them in the ring
@@ -59,9 +60,9 @@ struct Tc1 {
   static_assert(colP2 + (SPLIT - 1) * KT <= 512, "tensor memory");
 };
 
-template <typename T, int D>
+template <typename T, int D, bool PARTS>
 __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs a) {
-  using C = Tc1<T, D>;
+  using C = Tc1<T, D, PARTS>;
   constexpr int KT = C::KT, SPLIT = C::SPLIT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -215,6 +216,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
       // where the row's sum goes: the output, or this CTA's piece of it
       T* out = reinterpret_cast<T*>(a.out) + (live ? row_at() : 0);
       float* part = a.part_o + slot * D;
+      // fp32: the sum of the row's parts lies there as well; bf16: in memory of its own
+      auto sum_of_parts = [&]() {
+        if constexpr (SPLIT == 2)
+          return complete ? reinterpret_cast<float*>(out) : part;
+        else
+          return reinterpret_cast<float*>(a.sum_o) + ((int64_t)blockIdx.x * kTc1Rows + row) * D;
+      };
       float m = -INFINITY, mx = -INFINITY, l = 0.f;
       bool wild = false;
       // The reference that the other warpgroup left, m0 >= m.  Value exponents far apart
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
             const bool scaled = m - m0 > 60.f || m0 == -INFINITY;
             const float f = m0 == -INFINITY ? 0.f : fast_exp2(scaled ? m0 - m : m - m0);
             if (begin || scaled) mem_ref[row] = m;
-            float* sum = complete ? reinterpret_cast<float*>(out) : part;
+            float* sum = sum_of_parts();
             __syncwarp();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
           tmem_wait_ld();
         }
         if (in_memory && (live || !complete)) {
-          const float* sum = complete ? reinterpret_cast<const float*>(out) : part;
+          const float* sum = sum_of_parts();
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
             const float4 o = __ldcg(reinterpret_cast<const float4*>(sum + c + k));
@@ -600,15 +608,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
   if (warp == 12) tmem_dealloc(*tmem_sm, 512);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PARTS>
 csa_status launch_tc1(AttnArgs& a, cudaStream_t st) {
-  auto kern = kv8_attend_tc1_kernel<T, D>;
-  const int smem = Tc1<T, D>::total + 1024;
+  auto kern = kv8_attend_tc1_kernel<T, D, PARTS>;
+  const int smem = Tc1<T, D, PARTS>::total + 1024;
   if (!set_kernel_smem((const void*)kern, smem)) return CSA_ERR_CUDA;
   const long long items = (long long)a.E * a.H;
   long long grid = items;
   if (a.planned) {
-    const long long units = items * ((a.N + Tc1<T, D>::KT - 1) / Tc1<T, D>::KT);
+    const long long units = items * ((a.N + Tc1<T, D, PARTS>::KT - 1) / Tc1<T, D, PARTS>::KT);
     grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = units;
   }
@@ -633,8 +641,16 @@ int kv8_attend_tc1_rows() { return kTc1Rows; }
 
 csa_status launch_kv8_attend_tc1(const csa_kv8_params& p, AttnArgs& a, cudaStream_t st) {
   if (p.act == CSA_F32)
-    return p.d == 64 ? launch_tc1<float, 64>(a, st) : p.d == 128 ? launch_tc1<float, 128>(a, st) : launch_tc1<float, 256>(a, st);
-  return p.d == 64 ? launch_tc1<__nv_bfloat16, 64>(a, st) : p.d == 128 ? launch_tc1<__nv_bfloat16, 128>(a, st) : launch_tc1<__nv_bfloat16, 256>(a, st);
+    return p.d == 64    ? launch_tc1<float, 64, false>(a, st)
+           : p.d == 128 ? launch_tc1<float, 128, false>(a, st)
+                        : launch_tc1<float, 256, false>(a, st);
+  if (a.parts)
+    return p.d == 64    ? launch_tc1<__nv_bfloat16, 64, true>(a, st)
+           : p.d == 128 ? launch_tc1<__nv_bfloat16, 128, true>(a, st)
+                        : launch_tc1<__nv_bfloat16, 256, true>(a, st);
+  return p.d == 64    ? launch_tc1<__nv_bfloat16, 64, false>(a, st)
+         : p.d == 128 ? launch_tc1<__nv_bfloat16, 128, false>(a, st)
+                      : launch_tc1<__nv_bfloat16, 256, false>(a, st);
 }
 
 }  // namespace csa

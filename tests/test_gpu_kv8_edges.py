@@ -429,3 +429,65 @@ def test_attend_fp32_parts_when_the_reference_leaps(case):
         tol = tol + N * 2.0 ** -126 * 448 * 2.0 ** 20
     within(np64(out[some]), ref, tol, "out")
     assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------ bf16 sums over long caches --
+@pytest.mark.parametrize("B,Q,n_q,n_kv,N,rows", [(37, 1, 4, 4, 1 << 18, 16), (37, 1, 4, 4, 1 << 20, 16),
+                                                 (1, 592, 64, 4, 1 << 20, 256)])
+def test_attend_bf16_sums_drift_less_than_their_rounding(B, Q, n_q, n_kv, N, rows):
+    """What the tensor cores cut off an accumulator of values of one sign, one CTA an
+    item (0.8% over 1M slots without parts), stays below a quarter of bf16's step,
+    2^-10."""
+    d, block = 64, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    codes = torch.randint(0x30, 0x50, (2, B, n_kv, N, d), generator=g, device=DEV, dtype=torch.uint8)
+    exps = torch.full((2, B, n_kv, N // block), 125, dtype=torch.uint8, device=DEV)
+    q = (0.05 * torch.randn(B * Q, n_q, d, generator=g, device=DEV)).to(torch.bfloat16)
+    vis = torch.full((B * Q,), N - 9, dtype=torch.int32, device=DEV)
+    out = run_form(("bf16", B, Q, n_q, n_kv, d, N, rows), codes, exps, q, vis, block, d ** -0.5)
+    some = [0, B * Q // 2, B * Q - 1]
+    ref, _, _, _ = attend64(q[some], vis[some], codes[:, some] if B > 1 else codes, exps[:, some] if B > 1 else exps,
+                            block, d ** -0.5)
+    assert abs(drift_of(np64(out[some]), ref)) < 2.0 ** -10, drift_of(np64(out[some]), ref)
+
+
+RISING = [  # B, Q, n_q, n_kv, d, N, rows: whole items and items that CTAs share
+    (1, 592, 64, 4, 64, 131072, 256), (1, 500, 64, 4, 64, 131072, 256), (1, 592, 64, 4, 128, 131072, 256),
+    (1, 500, 64, 4, 128, 98304, 256), (1, 296, 64, 4, 256, 131072, 128), (1, 250, 64, 4, 256, 131072, 128),
+    (37, 2, 8, 4, 64, 1 << 19, 16)]
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("case", RISING, ids=[f"d{c[4]}-Q{c[1]}-N{c[5]}-rows{c[6]}" for c in RISING])
+def test_attend_bf16_parts_under_a_rising_reference(case, weights):
+    """Logits that rise with the slot: the sums of earlier parts count, scaled down."""
+    B, Q, n_q, n_kv, d, N, rows = case
+    block = 64
+    g = torch.Generator(device=DEV).manual_seed(10)
+    codes = torch.randint(0x30, 0x50, (2, B, n_kv, N, d), generator=g, device=DEV, dtype=torch.uint8)
+    codes[0, ..., 0] = torch.linspace(-440.0, 440.0, N, device=DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+    exps = torch.full((2, B, n_kv, N // block), 125, dtype=torch.uint8, device=DEV)
+    q = 0.02 * torch.randn(B * Q, n_q, d, generator=g, device=DEV)
+    q[..., 0] = 4.0 * d ** 0.5 / 110.0    # logits from -4 to 4
+    q = q.to(torch.bfloat16)
+    vis = (N - torch.arange(B * Q, device=DEV) % 100).to(torch.int32)
+    vis[1], vis[B * Q - 2] = 40000, 0
+    acc = torch.zeros(B, n_kv, N // block, device=DEV) if weights else None
+    p = bd.kv8_params(n_q, n_kv, d, block, N, "bf16")
+    out = torch.full_like(q, float("nan"))
+    with rows_of_a_cta(rows):
+        bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], out, acc=acc)
+    if B == 1:
+        some = torch.tensor([0, 1, 2, Q // 2, Q - 2, Q - 1], device=DEV)
+        ref, _, mag, load = attend64(q[some], vis[some], codes, exps, block, d ** -0.5)
+    else:
+        some = torch.tensor([0, 1, 34, 35, 72, 73], device=DEV)
+        b = some[::2] // Q
+        ref, _, mag, load = attend64(q[some], vis[some], codes[:, b], exps[:, b], block, d ** -0.5)
+    within(np64(out[some]), ref, attend_tol("bf16", d, N, ref, mag, load, load.max()), "out")
+    if weights:   # each row's weights add up to 1, summed in fp32 over its slots and the rows
+        rows_seen = (vis.view(B, Q) > 0).sum(1).double().cpu().numpy()[:, None] * (n_q // n_kv)
+        eps = (2 * d + 24) * U * load.max()
+        within(np64(acc).sum(-1), np.broadcast_to(rows_seen, (B, n_kv)),
+               (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * rows_seen, "acc")
+

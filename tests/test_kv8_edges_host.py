@@ -17,9 +17,18 @@ def lib():
 def test_a_plan_counts_units_in_32_bits():
     """1024 row tiles over 2^28 slots are 2^31 units of 128 slots: a plan (and the
     workspace of its pieces) for one tile less, a CTA a tile beyond."""
-    p = bd.kv8_params(1, 1, 64, 128, 1 << 28, "bf16")
-    assert bd.kv8_attend_workspace_bytes(p, 1, 1023 * 256) > 0
-    assert bd.kv8_attend_workspace_bytes(p, 1, 1024 * 256) == 0
+    p = bd.kv8_params(1, 1, 64, 128, 1 << 28, "f32")
+    assert bd.kv8_attend_workspace_bytes(p, 1, 1023 * 128) > 0
+    assert bd.kv8_attend_workspace_bytes(p, 1, 1024 * 128) == 0
+
+
+@pytest.mark.parametrize("d,N,B,Q", [(128, 1 << 16, 1, 200000), (64, 1 << 20, 300, 4096), (256, 1 << 17, 7, 33333),
+                                     (128, 1 << 28, 1, 1 << 18)])
+def test_workspace_of_long_prompts_does_not_grow_with_them(d, N, B, Q):
+    """bf16 prompts over more than 32K slots: the sums of a plan's CTAs, whatever the
+    number of row tiles."""
+    p = bd.kv8_params(64, 8, d, 128, N, "bf16")
+    assert 0 < bd.kv8_attend_workspace_bytes(p, B, Q) <= 160 << 20
 
 
 @pytest.mark.parametrize("n_q,n_kv,d,block,N,B,Q", [
