@@ -58,8 +58,7 @@ constexpr float kPShift = 11.f;
 // The tensor cores cut off what they add to an accumulator, towards zero: O of one
 // sign shrank by 3.6e-8 a product, 5e-5 over 128K slots; in parts by less than 4e-6.
 // It costs 1% (4 sequences of 1M, d = 128: 743 -> 747 us).  A sum in L2 cost 8%, every
-// product added to O by itself 19%.  bf16 outputs keep one accumulator: their own
-// rounding is 2^-9, a hundred times what 128K slots lose.
+// product added to O by itself 19%.  bf16, whose own rounding is 2^-9: after 512 tiles.
 constexpr int kPart = 16, kPartBf16 = 512;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -80,9 +79,10 @@ struct Cfg {
   // fp32: columns of tensor memory, D / 2 for a warp (four warps share the columns,
   // 32 lanes each)
   static constexpr int tmem_cols = D == 64 ? 128 : 256;
-  // the last sum is taken up in the loop or (d = 128) by code behind it: 16 sequences
-  // of 64K, 4 KV heads, d = 256: 463 and 504 us; 4 of 1M, d = 128: 817 and 743
-  static constexpr bool fold_last = D != 128;
+  // the last sum is taken up in the loop or (fp32, d = 128) by code behind it: fp32, 16
+  // sequences of 64K, 4 KV heads, d = 256: 463 and 504 us; 4 of 1M, d = 128: 817 and 743;
+  // bf16, 16 of 1M, 8 KV heads, d = 128: 5.63 and 5.72 ms
+  static constexpr bool fold_last = SPLIT == 1 || D != 128;
   static constexpr int ring = 0;
   static constexpr int qfrag = ring + NW * warp_ring;
   static constexpr int ml = qfrag + SPLIT * steps * 32 * 16;

@@ -27,7 +27,8 @@ constexpr int kTame = 40;
 // The tensor cores cut off what they add to an accumulator, towards zero, and of
 // products far below it all but a few bits.  bf16 prompts over values of one sign lost
 // 1.3e-4 over 32K slots, 9e-4 over 128K and 8e-3 over 1M: after so many slots of an
-// item O goes to a sum in memory and starts anew (0.8% of the time).
+// item O goes to a sum in memory and starts anew (256 queries over 1M slots, 64 heads, 8
+// KV heads, d = 128: 8.80 -> 9.14 ms; 512 over 128K 2.18 -> 2.24).
 constexpr int kPartSlots = 32768;
 
 struct AttnArgs {

@@ -54,6 +54,26 @@ struct Tc {
   static_assert(total + 1024 <= 232448, "shared memory");
 };
 
+// O of a row goes to its sum in memory: sum = f sum (nothing: `begin`) + O.  (Not inline:
+// registers of the loop around it would be spilled.)
+template <int D>
+__device__ __noinline__ void put_part(uint32_t tO, float4* sum, float f, bool begin) {
+  __syncwarp();
+  tmem_wait_st();  // O may just have been rescaled
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float w[16];
+    tmem_ld16(tO + c, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+      float4* at = sum + (c + k) / 4 * kTcRows;
+      const float4 o = begin ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(at);
+      *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
+    }
+  }
+}
+
 // PARTS: CTAs may walk more than kPartSlots slots of an item
 template <int D, bool PARTS>
 __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a) {
@@ -269,20 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc_kernel(AttnArgs a
             const float m0 = begin ? -INFINITY : mem_ref[st * 128 + row];
             const float f = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
             mem_ref[st * 128 + row] = m;
-            __syncwarp();
-            tmem_wait_st();  // O may just have been rescaled
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float w[16];
-              tmem_ld16(tO + c, w);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                float4* at = sum_at(c + k);
-                const float4 o = begin ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(at);
-                *at = make_float4(fmaf(o.x, f, w[k]), fmaf(o.y, f, w[k + 1]), fmaf(o.z, f, w[k + 2]), fmaf(o.w, f, w[k + 3]));
-              }
-            }
+            put_part<D>(tO, sum_at(0), f, begin);
           }
         }
         // the row's block weights from slot s0 on
