@@ -126,7 +126,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     fence_mbar_init();
   }
   pdl_wait();
-  pdl_trigger();
+  if constexpr (!PARTS) pdl_trigger();
   long long u0, u1;
   int e_base;
   Cursor cur;
@@ -139,6 +139,7 @@ kv8_attend_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_trigger();  // (not before: a dependent that takes tensor memory first would wait for this CTA, and it for that)
   }
   int issued = 0, used = 0;  // tiles of this warp so far
   uint8_t* my_ring = ring + warp * C::warp_ring;

@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
     fence_mbar_init();
   }
   pdl_wait();
-  pdl_trigger();
   long long u0, u1;
   int e_base;
   Cursor cur;
@@ -111,6 +110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();  // (not before: a dependent that takes tensor memory first would wait for this CTA, and it for that)
   // all 512 columns are this CTA's, so they start at 0
   if (*tmem_sm != 0) *abort_sm = 1;
 
