@@ -467,7 +467,15 @@ csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, 
  * n_vis[r] slots of its sequence and KV head; logits = scale * q . key, and
  * with sink != NULL the denominator also holds exp(sink_h) (the sink logit is
  * not scaled).  A row with n_vis <= 0 gives zeros.  Softmax statistics and
- * sums in fp32.
+ * sums in fp32, over long caches in parts (the tensor cores cut off what
+ * they add).  fp32 queries and the weights that multiply the values are held
+ * in two fp16 terms (22 bits); with bf16 activations these weights are one
+ * (11 bits; a quarter of the exponentials of prompts are off by up to
+ * 2.7e-6, which the accumulated weights share), below the output's own
+ * rounding.  They are held relative to the row's largest weight times its
+ * block's 2^e: where the values' exponents lie far apart, dims in which only
+ * blocks of small exponents have values are accurate to 2^-32 of that
+ * largest term (2^-36 with few rows a KV head), not to their own size.
  *   q       [B*Q][n_q][d]        act dtype
  *   n_vis   [B*Q] int32          slots each query sees (above N: clamped,
  *                                CSA_DEV_BAD_INDEX)
