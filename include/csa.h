@@ -471,7 +471,7 @@ csa_status csa_kv8_append(const csa_kv8_params* p, int B, int T, const void* k, 
  * they add).  fp32 queries and the weights that multiply the values are held
  * in two fp16 terms (22 bits); with bf16 activations these weights are one
  * (11 bits; a quarter of the exponentials of prompts are off by up to
- * 2.7e-6, which the accumulated weights share), below the output's own
+ * 2.9e-6, which the accumulated weights share), below the output's own
  * rounding.  They are held relative to the row's largest weight times its
  * block's 2^e: where the values' exponents lie far apart, dims in which only
  * blocks of small exponents have values are accurate to 2^-32 of that

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attend_tc1_kernel(AttnArgs 
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               const float2 z = fma2(make_float2(v[16 * g + k], v[16 * g + k + 1]), c, o);
-              // (the polynomial's 2.7e-6 is too much for two terms of fp16)
+              // (the polynomial's 2.9e-6 is too much for two terms of fp16)
               const float2 p = SPLIT == 1 && (k >> 1) % 4 == 3 ? exp2_poly(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
               s2[(k >> 1) & 1] = add2(s2[(k >> 1) & 1], p);
               const uint32_t hi = pack_h2(p.x, p.y);

@@ -491,3 +491,28 @@ def test_attend_bf16_parts_under_a_rising_reference(case, weights):
         within(np64(acc).sum(-1), np.broadcast_to(rows_seen, (B, n_kv)),
                (2 * eps + (N / 8 + 2 * block + Q * n_q // n_kv + 24) * U) * rows_seen, "acc")
 
+
+@pytest.mark.parametrize("case", [c for c in FORMS if c[2] > 3 and c[6] == 160] + [("bf16", 1, 250, 64, 4, 256, 160, 128)],
+                         ids=lambda c: f"{c[0]}-d{c[5]}-rows{c[7]}")
+def test_attend_weights_that_vanish_are_zero(case):
+    """The first block takes everything, by 2^200, and has the largest value
+    exponent; slots that weigh nothing, visible or masked, add nothing to acc."""
+    act, B, Q, n_q, n_kv, d, N, rows = case
+    g = torch.Generator().manual_seed(11)
+    block = 16
+    codes = ordinary_codes((2, B, n_kv, N, d), g, 1.0)
+    codes[0, ..., 0] = 0
+    codes[0, :, :, :block, 0] = 0x70          # 128
+    exps = torch.full((2, B, n_kv, N // block), 127, dtype=torch.uint8)
+    exps[1], exps[1, :, :, 0] = 87, 167
+    q = 0.1 * torch.randn(B * Q, n_q, d, generator=g)
+    q[..., 0] = 200.0 / 128 * np.log(2.0) * d ** 0.5
+    q, codes, exps = q.to(DT[act]).to(DEV), codes.to(DEV), exps.to(DEV)
+    vis = (block + 1 + torch.arange(B * Q, device=DEV) % (N - block)).to(torch.int32)
+    acc = torch.zeros(B, n_kv, N // block, device=DEV)
+    out = run_form(case, codes, exps, q, vis, block, d ** -0.5, acc=acc)
+    assert (acc[..., 0] - Q * n_q // n_kv).abs().max() < 1e-3 * Q * n_q // n_kv
+    assert acc[..., 1:].max() < 1e-45
+    ref, _, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5)
+    within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()) + N * 2.0 ** -32 * 448 * 2.0 ** 40, "out")
+
