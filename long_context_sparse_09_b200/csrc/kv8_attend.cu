@@ -7,9 +7,10 @@
 // c_n the value's codes: E4M3 codes are exact in fp16, so both products run
 // on codes as they are and every power of two goes into an exponent.  q is
 // held as fp16 times a power of two per row (bf16 queries exactly; fp32 ones
-// as two fp16 terms), p = 2^(y - M + 11) as one or two fp16 terms: the factor
-// 2^11 uses fp16's range up to 2^15, so p keeps 11 bits down to 2^-25 of the
-// row's largest term.
+// as two fp16 terms), p = 2^(y - M + 11) as one fp16 term or (fp32) two: the factor
+// 2^11 uses fp16's range up to 2^15, so a term keeps 11 bits down to 2^-25 of the
+// row's largest.  One term is off by 2^-11 of each weight at most, an eighth of bf16's
+// half step; a second would cost every product of P V once more.
 //
 // What bounds it: the bytes of the cache, read once.  A CTA of 12 warps (d = 64:
 // 16, d = 256: 6) works on one KV head and 16 query rows (heads of the group x
@@ -23,10 +24,11 @@
 // path's rate to keep up with HBM, and its operands come from registers, where
 // the codes are widened, without a way through shared or tensor memory.
 //
-// 4 sequences of 1M tokens, 64 heads, 4 KV heads, d = 128: 638 to 730 us on
-// different machines for 4.30 GB, 90 to 102% of the measured copy rate; 32 of up to
-// 64K tokens, 8 KV heads, with accumulated weights: 547 us for 3.26 GB (90%).  With
-// 8 warps 719 and 659: a warp's 600 instructions a tile, not the loads, were
+// 4 sequences of 1M tokens, 64 heads, 4 KV heads, d = 128: 709 to 766 us in long runs
+// on different machines for 4.30 GB, 85 to 92% of the measured copy rate (638 in
+// bursts, under the power limit); 32 of up to 64K tokens, 8 KV heads, with accumulated
+// weights: 605 to 646 us for 3.26 GB, 77 to 82% (547 in bursts).  fp32 747 and 860.  With
+// 8 warps 719 and 659 in bursts: a warp's 600 instructions a tile, not the loads, were
 // waited for (issue slots 37% busy; 45% now).  One sequence of 1,111 tokens: 10 us
 // in a graph, a chain of lengths (1.2), queries (1.6), 1.5 a unit, and the join
 // of the warps (1.9).
@@ -58,7 +60,7 @@ constexpr float kPShift = 11.f;
 // The tensor cores cut off what they add to an accumulator, towards zero: O of one
 // sign shrank by 3.6e-8 a product, 5e-5 over 128K slots; in parts by less than 4e-6.
 // It costs 1% (4 sequences of 1M, d = 128: 743 -> 747 us).  A sum in L2 cost 8%, every
-// product added to O by itself 19%.  bf16, whose own rounding is 2^-9: after 512 tiles.
+// product added to O by itself 19%.  bf16, whose half step is 2^-8: after 512 tiles.
 constexpr int kPart = 16, kPartBf16 = 512;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {

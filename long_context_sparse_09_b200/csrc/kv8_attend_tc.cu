@@ -13,19 +13,21 @@
 //         goes back as fp16 over the front half of S (all of S in registers
 //         spills: 2.9 ms instead of 2.2 at the size below)
 //   O_s += P_s V       tcgen05.mma, P from TMEM, V MN-major in shared memory
-// While a stream's softmax runs, the tensor cores work for the other one.  A
+// While a stream's softmax runs, the tensor cores can work for the other one.  A
 // third warpgroup widens the codes: 16-byte global loads (a tile ahead, in
 // registers) -> fp16 in the 128-byte swizzle layout, K and V tiles alternating
 // in one ring.  All tiles of the call lie on one line, cut evenly over the SMs;
 // the pieces of items that several CTAs share are joined by kv8_join.
 //
-// What bounds it: forming P.  The two softmax warps of a scheduler take 2,015
-// cycles a tile for their exponentials, sums and packing alone (measured without
-// products; 1,536 of them the special function unit's), 470 for the maxima, next
-// to 2,060 of products for both streams; without P the kernel takes 1.37 ms, with
-// half of it 1.50.  2048 queries of 64 heads over 32K slots of 8 KV heads (d = 128):
-// 2.17 ms, 980 TFLOP/s, 61% of the measured bf16 rate (2.39 in long runs, under the
-// power limit); on mma.sync (kv8_attend.cu) 11.4 ms.  Tiles of 64 slots with two S
+// What bounds it: the latency of a stream's chain S -> maximum -> P -> P V.  A pair of
+// tiles (both streams) takes 4,700 cycles; its products take 2,060 of the tensor cores,
+// the two softmax warps of a scheduler 2,015 for exponentials, sums and packing
+// (measured without products; 1,536 of them the special function unit's) and 470 for
+// the maxima, and they overlap only in part: no pipe is busy half of the time.
+// Without P the kernel takes 1.37 ms, with half of it 1.50.  2048 queries of 64 heads
+// over 32K slots of 8 KV heads (d = 128):
+// 2.17 ms, 980 TFLOP/s, 61% of the measured bf16 rate (2.39 to 2.42 in long runs, under
+// the power limit); on mma.sync (kv8_attend.cu) 11.4 ms.  Tiles of 64 slots with two S
 // buffers a stream took 2.49 ms (a product with N = 64 costs as much as one with N =
 // 128), the products issued by the softmax warps themselves 2.6 ms, four softmax
 // warpgroups of half a tile each 2.94.

@@ -14,11 +14,10 @@
 //
 // What bounds it: the softmax of a tile (about 3,000 cycles of one warpgroup, two
 // of them running) against its products.  The last 2048 queries over 8K slots, 64
-// heads, 8 KV heads: bf16, d = 256 1.17 ms (820
-// TFLOP/s), fp32, d = 128 1.02 ms (470 TFLOP/s of fp32 attention, twice that in fp16
-// products; 0.89 without the sums in parts), fp32, d = 64 0.78 ms; on mma.sync
-// (kv8_attend.cu) 5.2, 3.25 and 2.25 ms.  fp32 at d = 256 has room for one K and one
-// V tile only: 2.57 ms (mma.sync 6.7).
+// heads, 8 KV heads (cache not in L2): bf16, d = 256 1.18 ms (810 TFLOP/s); fp32, d = 128
+// 1.08 ms (450 TFLOP/s of fp32 attention, twice that in fp16 products; 14% of it the
+// sums in parts), d = 64 0.82 ms, d = 256, with room for one K and one V tile only,
+// 2.84 ms; on mma.sync (kv8_attend.cu; cache in L2) 5.2, 3.25, 2.25 and 6.7 ms.
 #include "kv8_attend_tc.cuh"
 
 namespace csa {

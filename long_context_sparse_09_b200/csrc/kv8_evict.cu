@@ -12,11 +12,11 @@
 //
 // What bounds it: the bytes of the blocks that move, read and written once, and
 // for short caches the chain of votes and scans of kv8_select.  8 sequences of
-// 64K tokens cut to half (8 KV heads, d = 128, blocks of 64): 70 us for 361 MB, 79%
-// of the measured copy rate (256 threads a block and one load of each cache in
-// flight: 88 us; 64 threads 74, 8 loads 89).  A cache with few blocks
-// beyond the budget is done in one kernel: 4 sequences, 125 blocks a head, one of
-// them to go, 10.6 us as a graph of one call (12.7 with kv8_move behind it).
+// 64K tokens cut to half (8 KV heads, d = 128, blocks of 64): 67 to 70 us for 361 MB,
+// 79 to 82% of the measured copy rate (256 threads a block and one load of each cache
+// in flight: 88 us; 64 threads 74, 8 loads 89).  A cache with few blocks beyond the
+// budget is done in one kernel: 4 sequences, 125 blocks a head, one of them to go,
+// 10.6 us as a graph of one call (12.7 with kv8_move behind it).
 #include "common.cuh"
 #include "kv8.h"
 

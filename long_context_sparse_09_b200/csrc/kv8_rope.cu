@@ -10,8 +10,8 @@
 // elsewhere the row goes through shared memory.
 //
 // What bounds it: for prompts the bytes, each read and written once; 32K tokens
-// of 64 + 8 heads (d = 128, bf16, 64 rotated dims) 208 us for 1.21 GB, 88% of the
-// measured copy rate.  For few tokens the chain position -> angles -> heads: four
+// of 64 + 8 heads (d = 128, bf16, 64 rotated dims) 208 to 216 us for 1.21 GB, by
+// machine, 85 to 88% of the measured copy rate.  For few tokens the chain position -> angles -> heads: four
 // tokens of 64 + 8 heads 3.0 us in a graph.
 #include "common.cuh"
 #include "kv8.h"

@@ -436,8 +436,8 @@ def test_attend_fp32_parts_when_the_reference_leaps(case):
                                                  (1, 592, 64, 4, 1 << 20, 256)])
 def test_attend_bf16_sums_drift_less_than_their_rounding(B, Q, n_q, n_kv, N, rows):
     """What the tensor cores cut off an accumulator of values of one sign, one CTA an
-    item (0.8% over 1M slots without parts), stays below a quarter of bf16's step,
-    2^-10."""
+    item (0.8% over 1M slots without parts), stays below a quarter of bf16's half
+    step, 2^-10."""
     d, block = 64, 64
     g = torch.Generator(device=DEV).manual_seed(9)
     codes = torch.randint(0x30, 0x50, (2, B, n_kv, N, d), generator=g, device=DEV, dtype=torch.uint8)
