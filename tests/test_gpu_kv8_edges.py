@@ -516,3 +516,44 @@ def test_attend_weights_that_vanish_are_zero(case):
     ref, _, mag, load = attend64(q, vis, codes, exps, block, d ** -0.5)
     within(np64(out), ref, attend_tol(act, d, N, ref, mag, load, load.max()) + N * 2.0 ** -32 * 448 * 2.0 ** 40, "out")
 
+
+# ------------------------------------------------------- long calls side by side --
+LONG = [  # act, B, Q, n_q, n_kv, d, block, N: sums in tensor memory, in memory, calls that run as several
+    ("f32", 37, 1, 8, 4, 128, 64, 16384), ("bf16", 1, 250, 64, 4, 128, 64, 98304),
+    ("bf16", 5, 500, 64, 8, 64, 16, 16384), ("f32", 1, 287, 64, 8, 64, 32, 6144)]
+
+
+def test_long_calls_captured_and_on_streams_of_their_own():
+    """Calls in parts, captured with a workspace each and replayed at the same time,
+    give the bits of the same calls alone."""
+    runs = []
+    for i, (act, B, Q, n_q, n_kv, d, block, N) in enumerate(LONG):
+        g = torch.Generator(device=DEV).manual_seed(12 + i)
+        p = bd.kv8_params(n_q, n_kv, d, block, N, act)
+        codes = torch.randint(0, 0x58, (2, B, n_kv, N, d), generator=g, device=DEV, dtype=torch.uint8)
+        exps = torch.full((2, B, n_kv, N // block), 121, dtype=torch.uint8, device=DEV)
+        q = (0.3 * torch.randn(B * Q, n_q, d, generator=g, device=DEV)).to(DT[act])
+        vis = (N - torch.arange(B * Q, device=DEV) % 300).to(torch.int32)
+        acc = torch.zeros(B, n_kv, N // block, device=DEV)
+        ws = torch.empty(bd.kv8_attend_workspace_bytes(p, B, Q, True), dtype=torch.uint8, device=DEV)
+        out, want, wacc = torch.empty_like(q), torch.empty_like(q), acc.clone()
+
+        def call(o, a, w=None, p=p, q=q, vis=vis, codes=codes, exps=exps):
+            bd.csa_kv8_attend(p, q, vis, codes[0], exps[0], codes[1], exps[1], o, acc=a, decay=0.5, workspace=w)
+        call(want, wacc)
+        s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=s):
+            call(out, acc, ws)
+        # (the graph reads these tensors at every replay: they have to live as long)
+        runs.append((s, graph, out, acc, want, wacc, (q, vis, codes, exps, ws)))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, graph, out, acc, *_ in runs:
+            with torch.cuda.stream(s):
+                acc.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, acc, want, wacc, _ in runs:
+        assert torch.equal(out, want) and torch.equal(acc, wacc)
+
