@@ -198,8 +198,10 @@ struct Pieces {
     total = (long long)a.plan[a.E] * a.H;
     grid = (int)min((long long)launched, total);
     U0 = (long long)a.plan[e] * a.H + (long long)h * units;
-    c0 = (int)(((U0 + 1) * grid - 1) / total);
-    c1 = (int)(((U0 + units) * grid - 1) / total);
+    // (clamped: a plan that another call overwrote, in a workspace that two of them share
+    // against the rules, gives wrong pieces but no address outside of the workspace)
+    c0 = (int)min(max(((U0 + 1) * grid - 1) / max(total, 1ll), 0ll), (long long)launched - 1);
+    c1 = (int)min(max(((U0 + units) * grid - 1) / max(total, 1ll), (long long)c0), (long long)launched - 1);
   }
   __device__ __forceinline__ int64_t slot(int c) const {
     return (int64_t)c * 2 + (cut(c, total, grid) >= U0 ? 0 : 1);
